@@ -2,8 +2,10 @@
 // stream. Nothing here allocates, frees or synchronises.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "velox_internal.cuh"
 
@@ -263,6 +265,301 @@ int velox_cast_bf16(const float* x, uint16_t* y, size_t n, void* stream) {
     if (!x || !y) return VELOX_EINVAL;
     if (n == 0) return VELOX_OK;
     return velox::cast_bf16_launch(x, y, n, as_stream(stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr long long INT_LIMIT = 1ll << 31;
+
+inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// Fills the rotation of a launch; `rope` may be NULL (nothing is rotated).
+int set_rope(velox::RopeArgs& r, const velox_rope_t* rope, int d, const int32_t* pos) {
+    if (!rope) {
+        r.rot = 0;
+        r.axes = 1;
+        r.half_style = 1;
+        return VELOX_OK;
+    }
+    if (rope->style != VELOX_ROPE_HALF && rope->style != VELOX_ROPE_INTERLEAVED)
+        return VELOX_EUNSUPPORTED;
+    if (rope->rot < 0 || rope->rot > d || rope->rot % 2 || rope->axes < 1 || rope->axes > 3)
+        return VELOX_EINVAL;
+    long long sum = 0;
+    for (int i = 0; i < rope->axes; ++i) {
+        if (rope->sections[i] < 0) return VELOX_EINVAL;
+        sum += rope->sections[i];
+    }
+    if (sum != rope->rot / 2 || !std::isfinite(rope->mscale)) return VELOX_EINVAL;
+    if (rope->rot > 0 && (!rope->freqs || !pos || !aligned(rope->freqs, 8) || !aligned(pos, 4)))
+        return VELOX_EINVAL;
+    r.rot = rope->rot;
+    r.half_style = rope->style == VELOX_ROPE_HALF;
+    r.axes = rope->axes;
+    // first pair of axis 1 and of axis 2; an axis that is not there begins behind the last pair
+    r.sec0 = rope->sections[0];
+    r.sec01 = rope->axes > 1 ? rope->sections[0] + rope->sections[1] : rope->rot / 2;
+    r.freqs = rope->freqs;
+    r.pos = pos;
+    r.mscale = rope->mscale;
+    r.sign = rope->inverse ? -1.0f : 1.0f;
+    return VELOX_OK;
+}
+
+// 16-byte accesses of 8 elements: every row starts on 16 bytes, and the rotated
+// part is whole chunks (chunk pairs in the half layout)
+bool vec_rows(const void* p, int esize, int64_t s0, int64_t s1, int64_t s2) {
+    const int64_t step = 16 / esize;
+    return aligned(p, 16) && s0 % step == 0 && s1 % step == 0 && s2 % step == 0;
+}
+bool vec_rope(const velox::RopeArgs& r) {
+    return r.d % 8 == 0 && r.rot % (r.half_style ? 16 : 8) == 0;
+}
+
+int paged_plan_check(const void* a, const void* b, const void* c, const void* d, const void* e,
+                     const void* f, const void* g, int R, int max_pages, int page, int num_pages) {
+    for (const void* p : {a, b, c, d, e, f, g})
+        if (!p || !aligned(p, 4)) return VELOX_EINVAL;
+    if (R < 1 || R > 8192 || page < 1 || max_pages < 1 || num_pages < 1) return VELOX_EINVAL;
+    if (!page_ok(page)) return VELOX_EUNSUPPORTED;
+    if (static_cast<long long>(max_pages) * page >= INT_LIMIT ||
+        static_cast<long long>(num_pages) * page >= INT_LIMIT)
+        return VELOX_EINVAL;
+    return VELOX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int velox_rope_freqs(int rot, double base, int kind, double factor, int orig_len,
+                     double beta_fast, double beta_slow, double* freqs, float* mscale) {
+    if (!freqs || rot < 2 || rot % 2) return VELOX_EINVAL;
+    if (kind < VELOX_ROPE_PLAIN || kind > VELOX_ROPE_BANDS) return VELOX_EUNSUPPORTED;
+    if (!std::isfinite(base) || !(base > 1.0)) return VELOX_EINVAL;
+    if (kind != VELOX_ROPE_PLAIN && (!std::isfinite(factor) || !(factor >= 1.0)))
+        return VELOX_EINVAL;
+    if (kind == VELOX_ROPE_BASE) {
+        if (rot == 2) return VELOX_EINVAL;
+        base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+        if (!std::isfinite(base)) return VELOX_EINVAL;
+    }
+    double low = 0.0, high = 1.0;
+    if (kind == VELOX_ROPE_BANDS) {
+        if (orig_len < 1 || !std::isfinite(beta_fast) || !(beta_slow > 0.0) ||
+            !(beta_fast > beta_slow))
+            return VELOX_EINVAL;
+        // pair index that makes n turns over orig_len positions
+        const auto index = [&](double n) {
+            return rot * std::log(orig_len / (n * 6.283185307179586)) / (2.0 * std::log(base));
+        };
+        low = std::min(std::max(std::floor(index(beta_fast)), 0.0), rot - 1.0);
+        high = std::min(std::max(std::ceil(index(beta_slow)), 0.0), rot - 1.0);
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot);
+        double slow = 0.0;  // share of f / factor
+        if (kind == VELOX_ROPE_LINEAR) slow = 1.0;
+        if (kind == VELOX_ROPE_BANDS)
+            slow = high > low ? std::min(std::max((i - low) / (high - low), 0.0), 1.0)
+                              : (i > low ? 1.0 : 0.0);
+        freqs[i] = slow == 0.0 ? f : f * (1.0 - slow) + f / factor * slow;
+    }
+    if (mscale)
+        *mscale = kind == VELOX_ROPE_BANDS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return VELOX_OK;
+}
+
+int velox_rope(const void* x, int dtype, int B, int H, int N, int d, const int64_t* xs,
+               const int32_t* pos, int64_t pos_axis_stride, int64_t pos_batch_stride,
+               const velox_rope_t* rope, void* y, const int64_t* ys, void* stream) {
+    if (!x || !y || !rope || !xs || !ys) return VELOX_EINVAL;
+    if (dtype != VELOX_BF16 && dtype != VELOX_F32) return VELOX_EUNSUPPORTED;
+    if (B < 1 || H < 1 || N < 1 || d < 1 || d > 4096) return VELOX_EINVAL;
+    if (static_cast<long long>(B) * N >= INT_LIMIT) return VELOX_EINVAL;
+    const int esize = dtype == VELOX_BF16 ? 2 : 4;
+    if (!aligned(x, esize) || !aligned(y, esize)) return VELOX_EINVAL;
+    const int dims[3] = {B, H, N};
+    for (int i = 0; i < 3; ++i)
+        if (xs[i] < 0 || ys[i] < 0 || (ys[i] == 0 && dims[i] > 1)) return VELOX_EINVAL;
+
+    velox::RopeArgs r{};
+    const int rc = set_rope(r, rope, d, pos);
+    if (rc != VELOX_OK) return rc;
+    r.groups = 1;
+    r.rows = H;
+    r.rotated_rows = r.rot > 0 ? H : 0;
+    r.tokens = static_cast<long long>(B) * N;
+    r.N = N;
+    r.d = d;
+    r.pos_axis = pos_axis_stride;
+    r.pos_batch = pos_batch_stride;
+    velox::RopeGroup& g = r.g[0];
+    g.x = x;
+    g.y = y;
+    g.heads = H;
+    g.rotate = 1;
+    g.xb = xs[0], g.xh = xs[1], g.xn = xs[2];
+    g.yb = ys[0], g.yh = ys[1], g.yn = ys[2];
+    const bool vec = vec_rope(r) && vec_rows(x, esize, xs[0], xs[1], xs[2]) &&
+                     vec_rows(y, esize, ys[0], ys[1], ys[2]);
+    return velox::rope_launch(r, dtype, false, vec, as_stream(stream));
+}
+
+int velox_paged_append(const void* q, const void* k, const void* v, int dtype, int N, int H,
+                       int Hkv, int d, const int64_t* qs, const int64_t* ks, const int64_t* vs,
+                       const int32_t* slots, const int32_t* pos, int64_t pos_axis_stride,
+                       const velox_rope_t* rope, void* q_out, void* k_pages, void* v_pages, int page,
+                       int num_pages, int32_t* status, void* stream) {
+    if (!k || !v || !ks || !vs || !slots || !k_pages || !v_pages) return VELOX_EINVAL;
+    if ((q == nullptr) != (q_out == nullptr) || (q && !qs)) return VELOX_EINVAL;
+    if (dtype != VELOX_BF16 && dtype != VELOX_F32) return VELOX_EUNSUPPORTED;
+    if (N < 1 || Hkv < 1 || (q && H < 1) || d < 1 || page < 1 || num_pages < 1)
+        return VELOX_EINVAL;
+    if (!page_ok(page) || !tile_ok(d)) return VELOX_EUNSUPPORTED;
+    const long long n_slots = static_cast<long long>(num_pages) * page;
+    if (n_slots >= INT_LIMIT || static_cast<long long>(q ? H : 0) + 2ll * Hkv >= INT_LIMIT)
+        return VELOX_EINVAL;
+    const int esize = dtype == VELOX_BF16 ? 2 : 4;
+    if (!aligned(k, esize) || !aligned(v, esize) || (q && !aligned(q, esize))) return VELOX_EINVAL;
+    if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || (q && !aligned(q_out, 16)) ||
+        !aligned(slots, 4))
+        return VELOX_EINVAL;
+    for (int i = 0; i < 2; ++i)
+        if (ks[i] < 0 || vs[i] < 0 || (q && qs[i] < 0)) return VELOX_EINVAL;
+
+    velox::RopeArgs r{};
+    const int rc = set_rope(r, rope, d, pos);
+    if (rc != VELOX_OK) return rc;
+    r.tokens = N;
+    r.N = N;
+    r.d = d;
+    r.pos_axis = pos_axis_stride;
+    r.slots = slots;
+    r.page = page;
+    for (r.page_shift = 4; (1 << r.page_shift) < page; ++r.page_shift) {}
+    r.n_slots = n_slots;
+    r.status = status;
+    bool vec = vec_rope(r);
+    const auto add = [&](const void* x, const int64_t* s, int heads, int rotate, void* y,
+                         bool to_pages) {
+        velox::RopeGroup& g = r.g[r.groups++];
+        g.x = x;
+        g.y = y;
+        g.heads = heads;
+        g.rotate = rotate;
+        g.to_pages = to_pages;
+        g.xn = s[0], g.xh = s[1];
+        g.yn = static_cast<long long>(heads) * d, g.yh = d;
+        r.rows += heads;
+        if (rotate) r.rotated_rows += heads;
+        vec = vec && vec_rows(x, esize, s[0], s[1], 0);
+    };
+    const int rotate = r.rot > 0;
+    if (q) add(q, qs, H, rotate, q_out, false);
+    add(k, ks, Hkv, rotate, k_pages, true);
+    add(v, vs, Hkv, 0, v_pages, true);
+    return velox::rope_launch(r, dtype, true, vec, as_stream(stream));
+}
+
+int velox_paged_plan(const int32_t* add, const int32_t* lens, int32_t* table,
+                     const int32_t* free_list, const int32_t* free_count, int R, int max_pages,
+                     int page, int num_pages, int n_cap, int32_t* lens_out,
+                     int32_t* free_count_out, int32_t* cu, int32_t* slots, int32_t* pos,
+                     int32_t* req, int32_t* status, void* stream) {
+    const int rc = paged_plan_check(add, lens, table, free_list, free_count, lens_out,
+                                    free_count_out, R, max_pages, page, num_pages);
+    if (rc != VELOX_OK) return rc;
+    if (!cu || n_cap < 0 || (n_cap > 0 && !slots)) return VELOX_EINVAL;
+    velox::PlanArgs a{};
+    a.add = add;
+    a.lens = lens;
+    a.table = table;
+    a.free_list = const_cast<int32_t*>(free_list);
+    a.free_count = free_count;
+    a.R = R;
+    a.max_pages = max_pages;
+    a.page = page;
+    a.num_pages = num_pages;
+    a.n_cap = n_cap;
+    a.lens_out = lens_out;
+    a.free_count_out = free_count_out;
+    a.cu = cu;
+    a.slots = slots;
+    a.pos = pos;
+    a.req = req;
+    a.status = status;
+    return velox::paged_plan_launch(a, as_stream(stream));
+}
+
+int velox_paged_release(const int32_t* done, const int32_t* lens, const int32_t* table,
+                        int32_t* free_list, const int32_t* free_count, int R, int max_pages,
+                        int page, int num_pages, int32_t* lens_out, int32_t* free_count_out,
+                        int32_t* status, void* stream) {
+    const int rc = paged_plan_check(done, lens, table, free_list, free_count, lens_out,
+                                    free_count_out, R, max_pages, page, num_pages);
+    if (rc != VELOX_OK) return rc;
+    velox::PlanArgs a{};
+    a.add = done;
+    a.lens = lens;
+    a.table = const_cast<int32_t*>(table);
+    a.free_list = free_list;
+    a.free_count = free_count;
+    a.R = R;
+    a.max_pages = max_pages;
+    a.page = page;
+    a.num_pages = num_pages;
+    a.lens_out = lens_out;
+    a.free_count_out = free_count_out;
+    a.status = status;
+    return velox::paged_release_launch(a, as_stream(stream));
+}
+
+size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d) {
+    if (R < 1 || R > 65535 || Hkv < 1 || H < Hkv || H % Hkv || !tile_ok(d)) return 0;
+    return velox::paged_attn_ws_bytes(R, H, Hkv, d);
+}
+
+int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
+                     const int32_t* lens, int R, int H, int Hkv, int d, int page, int num_pages,
+                     int max_pages, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                     int32_t* status, void* stream) {
+    if (!q || !k_pages || !v_pages || !table || !lens || !o || !ws) return VELOX_EINVAL;
+    if (R < 1 || R > 65535 || Hkv < 1 || H < Hkv || H % Hkv || d < 1 || page < 1 ||
+        num_pages < 1 || max_pages < 1)
+        return VELOX_EINVAL;
+    if (!tile_ok(d) || !page_ok(page)) return VELOX_EUNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
+        !aligned(ws, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+        return VELOX_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return VELOX_EINVAL;
+    // in this order no product leaves 63 bits
+    if (static_cast<long long>(max_pages) * page >= INT_LIMIT ||
+        static_cast<long long>(num_pages) * page >= INT_LIMIT ||
+        static_cast<long long>(num_pages) * page * Hkv >= INT_LIMIT ||
+        static_cast<long long>(R) * H >= INT_LIMIT)
+        return VELOX_EINVAL;
+    if (ws_bytes < velox_paged_attn_workspace_size(R, H, Hkv, d)) return VELOX_EINVAL;
+
+    velox::PagedAttnArgs a{};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.table = table;
+    a.lens = lens;
+    a.R = R;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.page = page;
+    a.num_pages = num_pages;
+    a.max_pages = max_pages;
+    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    a.part = static_cast<float*>(ws);
+    a.status = status;
+    a.wait_ns = velox::WAIT_LIMIT_NS;
+    return velox::paged_attn_launch(k_pages, v_pages, a, d, as_stream(stream));
 }
 
 }  // extern "C"

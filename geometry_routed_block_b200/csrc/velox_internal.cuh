@@ -65,6 +65,76 @@ int route_launch(const void* q, const void* k, int dtype, const RouteArgs& r, cu
 int kbar_append_launch(const void* k, int dtype, int BH, int Nk, int Nq, int d, int T, int chunk,
                        int cap, float* kbar, cudaStream_t st);
 
+// Rows of heads that a rotary launch handles: x is read, rotated (or only
+// copied) and written to `y` (dense or strided) or, with `pages`, to the slots
+// of a paged cache.
+struct RopeGroup {
+    const void* x;
+    void* y;
+    int heads;
+    int rotate;
+    int to_pages;
+    long long xb, xh, xn;  // elements between batches, heads, tokens
+    long long yb, yh, yn;  // the same of y (unused with to_pages)
+};
+struct RopeArgs {
+    RopeGroup g[3];
+    int groups;
+    int rows;          // heads of all groups
+    int rotated_rows;  // heads of the leading groups that are rotated
+    long long tokens;
+    int N;     // tokens per batch
+    int d, rot, half_style, axes, sec0, sec01;
+    const double* freqs;
+    const int32_t* pos;
+    long long pos_axis, pos_batch;
+    float mscale, sign;
+    const int32_t* slots;  // of the paged groups
+    int page, page_shift;
+    long long n_slots;
+    int32_t* status;
+};
+// in_dtype / out_bf16 (else float32); vec: 16-byte accesses are possible throughout
+int rope_launch(const RopeArgs& a, int in_dtype, bool out_bf16, bool vec, cudaStream_t st);
+
+struct PlanArgs {
+    const int32_t* add;   // plan: new tokens; release: requests that end
+    const int32_t* lens;
+    int32_t* table;
+    int32_t* free_list;
+    const int32_t* free_count;
+    int R, max_pages, page, num_pages, n_cap;
+    int32_t* lens_out;
+    int32_t* free_count_out;
+    int32_t* cu;
+    int32_t* slots;
+    int32_t* pos;
+    int32_t* req;
+    int32_t* status;
+};
+int paged_plan_launch(const PlanArgs& a, cudaStream_t st);
+int paged_release_launch(const PlanArgs& a, cudaStream_t st);
+
+struct PagedAttnArgs {
+    const __nv_bfloat16* q;
+    const int32_t* table;
+    const int32_t* lens;
+    int R, H, Hkv, page, num_pages, max_pages;
+    int group;       // query heads per key head
+    int head_tiles;  // tiles of at most 16 query heads per key head
+    int tile_heads;  // query heads per tile
+    int grid;        // CTAs that share the work
+    float scale_log2;
+    __nv_bfloat16* o;
+    float* lse;
+    float* part;     // workspace: partial results
+    int32_t* status;
+    unsigned long long wait_ns;
+};
+size_t paged_attn_ws_bytes(int R, int H, int Hkv, int d);
+int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnArgs& a, int d,
+                      cudaStream_t st);
+
 int cast_bf16_launch(const float* x, uint16_t* y, size_t n, cudaStream_t st);
 int fp64_fma_launch(double* out, int blocks, int threads, int iters, cudaStream_t st);
 

@@ -11,9 +11,11 @@ znear, zfar.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -27,13 +29,24 @@ VELOX_ETIMEOUT = -4
 VELOX_EBOUNDS = -5
 VELOX_STATUS_BAD_INDEX = 1
 VELOX_STATUS_TIMEOUT = 2
+VELOX_STATUS_NO_SPACE = 4
 VELOX_TEST_SKIP_MMA = 1
 VELOX_TEST_FORCE_PAIR = 2
 VELOX_BF16 = 0
 VELOX_F32 = 1
 CAM_FLOATS = 18
+ROPE_STYLES = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 _c_int, _c_size, _vp, _c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+_c_i64, _c_double = ctypes.c_int64, ctypes.c_double
+
+
+class _Rope(ctypes.Structure):
+    """velox_rope_t"""
+    _fields_ = [("freqs", _vp), ("rot", _c_int), ("style", _c_int), ("axes", _c_int),
+                ("sections", _c_int * 3), ("mscale", _c_float), ("inverse", _c_int)]
+
 
 # name -> (restype, argtypes); mirrors include/velox.h
 SIGNATURES = {
@@ -63,6 +76,17 @@ SIGNATURES = {
     "velox_route_topk_cached": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                          _c_int, _c_int, _vp, _c_float, _c_int, _vp, _vp, _c_size,
                                          _vp, _vp]),
+    "velox_rope_freqs": (_c_int, [_c_int, _c_double, _c_int, _c_double, _c_int, _c_double, _c_double,
+                                  _vp, _vp]),
+    "velox_rope": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_i64, _c_i64,
+                            _vp, _vp, _vp, _vp]),
+    "velox_paged_plan": (_c_int, [_vp] * 5 + [_c_int] * 5 + [_vp] * 8),
+    "velox_paged_release": (_c_int, [_vp] * 5 + [_c_int] * 4 + [_vp] * 4),
+    "velox_paged_append": (_c_int, [_vp] * 3 + [_c_int] * 5 + [_vp] * 5 + [_c_i64] + [_vp] * 4
+                           + [_c_int, _c_int, _vp, _vp]),
+    "velox_paged_attn_workspace_size": (_c_size, [_c_int] * 4),
+    "velox_paged_attn": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size, _vp,
+                                                             _vp]),
 }
 
 
@@ -336,3 +360,289 @@ def depth_multiwarp_noalloc(past_depth: torch.Tensor, past_cams: torch.Tensor,
                                              Hp, Wp, float(rel_tol), _ptr(out), _stream(stream)),
            "velox_depth_multiwarp_noalloc")
     return out
+
+
+# ---------------------------------------------------------------- tokens: rotary positions, paged cache
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _guard(x: torch.Tensor, stream):
+    """Where a call on x runs: x's device, and `stream` if one is given. Outputs
+    and scratch are allocated inside, so that they belong to that stream."""
+    if not x.is_cuda:
+        raise ValueError("libvelox takes CUDA tensors")
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+        return torch.cuda.stream(stream)
+    if x.device.index != torch.cuda.current_device():
+        return torch.cuda.device(x.device)
+    return _NO_GUARD
+
+
+def _arg(t: torch.Tensor | None, name: str, dtype: torch.dtype | None, shape: tuple | None,
+         device: torch.device, dense: bool = True):
+    """The address of an argument after its type, shape, device and layout have been looked at."""
+    if t is None:
+        return None
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str) -> tuple:
+    """The strides of a tensor whose innermost dimension is dense, 0 along dimensions of size 1."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()))
+
+
+def _in_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return VELOX_BF16
+    if t.dtype == torch.float32:
+        return VELOX_F32
+    raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+
+
+def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse: bool,
+               device: torch.device) -> _Rope:
+    if style not in ROPE_STYLES:
+        raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
+    if freqs.dim() != 1:
+        raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
+    sections = (freqs.shape[0],) if sections is None else tuple(int(s) for s in sections)
+    if not 1 <= len(sections) <= 3:
+        raise ValueError("one to three position axes")
+    return _Rope(_arg(freqs, "freqs", torch.float64, None, device), 2 * freqs.shape[0],
+                 ROPE_STYLES[style], len(sections),
+                 (_c_int * 3)(*sections), float(mscale), int(bool(inverse)))
+
+
+def _pos_shape(pos: torch.Tensor, axes: int, N: int, B: int | None) -> tuple:
+    """The shape that positions must have: [N] (one axis), [axes,N] or, with batches, [axes,B,N]."""
+    if pos.dim() == 1 and axes == 1:
+        return (N,)
+    return (axes, B, N) if pos.dim() == 3 and B is not None else (axes, N)
+
+
+def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Frequencies of `rot` rotated elements: ([rot/2] float64 radians per position,
+    mscale). scaling "linear", "base" and "bands" stretch the positions `factor` times
+    (include/velox.h states the formulas). For several axes, concatenate one
+    call's frequencies per axis."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (_c_double * max(1, rot // 2))()
+    m = _c_float(1.0)
+    _check(lib.velox_rope_freqs(int(rot), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                int(orig_len), float(beta_fast), float(beta_slow),
+                                ctypes.addressof(out), ctypes.addressof(m)), "velox_rope_freqs")
+    return torch.tensor(list(out), dtype=torch.float64).to(device), m.value
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "half",
+         sections=None, mscale: float = 1.0, inverse: bool = False,
+         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of x [B,H,N,d] (bf16 or f32; any strides, the last dimension
+    dense) -> the same shape and type. pos int32 [N] (one axis), [axes,N] or
+    [axes,B,N]; freqs [rot/2] float64; sections: pairs of each axis (default: one axis).
+    inverse turns back (which is also the gradient of the forward call); out may
+    be x itself."""
+    B, H, N, d = x.shape
+    dt = _in_dtype(x, "x")
+    spec = _rope_spec(freqs, style, sections, mscale, inverse, x.device)
+    p = _arg(pos, "pos", torch.int32, _pos_shape(pos, spec.axes, N, B), x.device)
+    batched = pos.dim() == 3
+    xs = _rows(x, "x")
+    with _guard(x, stream):
+        if out is None:
+            out = torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
+        y = _arg(out, "out", x.dtype, (B, H, N, d), x.device, dense=False)
+        ys = _rows(out, "out")
+        if y == x.data_ptr() and ys != xs:
+            raise ValueError("out may be x itself, not another view of it")
+        _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, (_c_i64 * 3)(*xs), p,
+                              B * N if batched else N, N if batched else 0,
+                              ctypes.byref(spec), y, (_c_i64 * 3)(*ys), _stream()), "velox_rope")
+    return out
+
+
+class PagedPlan(NamedTuple):
+    """What a step's requests and tokens look like: cu [R+1] first token of each
+    request, slots / pos / req [n_cap] of each token (-1: padding), lens [R] and
+    free_count [1] after the step."""
+    cu: torch.Tensor
+    slots: torch.Tensor
+    pos: torch.Tensor
+    req: torch.Tensor
+    lens: torch.Tensor
+    free_count: torch.Tensor
+
+
+def _pages_state(lens, table, free_list, free_count):
+    """Checks the state of a paged cache; (R, max_pages, num_pages, device, addresses)."""
+    dev = lens.device
+    if lens.dim() != 1 or table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("lens [R], table [R,max_pages], free_list [num_pages]")
+    R, i32 = lens.shape[0], torch.int32
+    if table.shape[0] != R:
+        raise ValueError(f"table has {table.shape[0]} rows for {R} requests")
+    ptrs = (_arg(lens, "lens", i32, None, dev), _arg(table, "table", i32, None, dev),
+            _arg(free_list, "free_list", i32, None, dev),
+            _arg(free_count, "free_count", i32, (1,), dev))
+    return R, table.shape[1], free_list.shape[0], dev, ptrs
+
+
+def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_list: torch.Tensor,
+               free_count: torch.Tensor, page: int, n_cap: int, out: PagedPlan | None = None,
+               status: torch.Tensor | None = None, stream=None) -> PagedPlan:
+    """Pages for add [R] new tokens of requests with lens [R] cached ones: enters
+    them in table [R,max_pages] and returns the step's PagedPlan with room for n_cap
+    tokens (all int32). `out` gives the outputs' tensors; its lens and
+    free_count may be the inputs, so that a captured step carries its state on."""
+    R, max_pages, num_pages, dev, (pl, pt, pf, pc) = _pages_state(lens, table, free_list, free_count)
+    i32 = torch.int32
+    pa = _arg(add, "add", i32, (R,), dev)
+    ps = _arg(status, "status", i32, None, dev)
+    n_cap = int(n_cap)
+    if not 0 <= n_cap < 2 ** 31:
+        raise ValueError("n_cap must be in [0, 2^31)")
+    with _guard(lens, stream):
+        if out is None:
+            e = lambda n: torch.empty(n, dtype=i32, device=dev)  # noqa: E731
+            out = PagedPlan(e(R + 1), e(n_cap), e(n_cap), e(n_cap), e(R), e(1))
+        o = [_arg(t, name, i32, (size,), dev) for t, name, size in
+             zip(out, PagedPlan._fields, (R + 1, n_cap, n_cap, n_cap, R, 1))]
+        _check(lib.velox_paged_plan(pa, pl, pt, pf, pc, R, max_pages, int(page), num_pages, n_cap,
+                                    o[4], o[5], o[0], o[1], o[2], o[3], ps, _stream()),
+               "velox_paged_plan")
+    return out
+
+
+def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                  free_list: torch.Tensor, free_count: torch.Tensor, page: int,
+                  lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+                  status: torch.Tensor | None = None, stream=None):
+    """The pages of the requests with done [R] != 0 go back on free_list (in
+    place); returns (lens, free_count) afterwards. The outputs may be the inputs."""
+    R, max_pages, num_pages, dev, (pl, pt, pf, pc) = _pages_state(lens, table, free_list, free_count)
+    i32 = torch.int32
+    pd = _arg(done, "done", i32, (R,), dev)
+    ps = _arg(status, "status", i32, None, dev)
+    with _guard(lens, stream):
+        if lens_out is None:
+            lens_out = torch.empty(R, dtype=i32, device=dev)
+        if free_count_out is None:
+            free_count_out = torch.empty(1, dtype=i32, device=dev)
+        _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, max_pages, int(page), num_pages,
+                                       _arg(lens_out, "lens_out", i32, (R,), dev),
+                                       _arg(free_count_out, "free_count_out", i32, (1,), dev), ps,
+                                       _stream()), "velox_paged_release")
+    return lens_out, free_count_out
+
+
+def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: torch.device):
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages,Hkv,page,d]")
+    return (_arg(k_pages, "k_pages", torch.bfloat16, None, device),
+            _arg(v_pages, "v_pages", torch.bfloat16, tuple(k_pages.shape), device))
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
+                 v_pages: torch.Tensor, q: torch.Tensor | None = None,
+                 pos: torch.Tensor | None = None, freqs: torch.Tensor | None = None,
+                 style: str = "half", sections=None, mscale: float = 1.0,
+                 out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """Writes k, v [N,Hkv,d] (bf16 or f32; any strides, the last dimension dense)
+    to their slots [N] int32 (negative: padding) of k_pages / v_pages
+    [num_pages,Hkv,page,d] bf16, in place. With freqs (see rope) k and q
+    [N,H,d] are rotated to pos [axes,N] int32 ([N] for one axis) on the way.
+    Returns q as bf16 [N,H,d], or None without q."""
+    N, Hkv, d = k.shape
+    dev = k.device
+    dt = _in_dtype(k, "k")
+    kp, vp = _pool(k_pages, v_pages, dev)
+    num_pages, hp, page, dp = k_pages.shape
+    if (hp, dp) != (Hkv, d):
+        raise ValueError(f"k has {Hkv} heads of {d}, the pages {hp} of {dp}")
+    pv = _arg(v, "v", k.dtype, (N, Hkv, d), dev, dense=False)
+    psl = _arg(slots, "slots", torch.int32, (N,), dev)
+    ps = _arg(status, "status", torch.int32, None, dev)
+    ks, vs = (_c_i64 * 2)(*_rows(k, "k")), (_c_i64 * 2)(*_rows(v, "v"))
+    spec = pp = None
+    if freqs is not None:
+        spec = _rope_spec(freqs, style, sections, mscale, False, dev)
+        if pos is None:
+            raise ValueError("freqs without pos")
+        pp = _arg(pos, "pos", torch.int32, _pos_shape(pos, spec.axes, N, None), dev)
+    H, pq, qs = 0, None, None
+    if q is not None:
+        H = q.shape[1]
+        pq = _arg(q, "q", k.dtype, (N, H, d), dev, dense=False)
+        qs = (_c_i64 * 2)(*_rows(q, "q"))
+    elif out is not None:
+        raise ValueError("out without q")
+    with _guard(k, stream):
+        if q is not None and out is None:
+            out = torch.empty((N, H, d), dtype=torch.bfloat16, device=dev)
+        po = _arg(out, "out", torch.bfloat16, (N, H, d), dev)
+        if po is not None and po == pq and (q.dtype != torch.bfloat16 or not q.is_contiguous()):
+            raise ValueError("out may be q itself only where q is contiguous bf16")
+        _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
+                                      ctypes.byref(spec) if spec is not None else None, po, kp, vp,
+                                      page, num_pages, ps, _stream()), "velox_paged_append")
+    return out
+
+
+def paged_attn_workspace(R: int, H: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
+    n = lib.velox_paged_attn_workspace_size(R, H, Hkv, d)
+    if n == 0:
+        raise VeloxError("velox_paged_attn_workspace_size", VELOX_EINVAL)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+               lens: torch.Tensor, scale: float | None = None, want_lse: bool = True,
+               ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """One new token per request, q [R,H,d] bf16, against its first lens [R] tokens
+    in k_pages / v_pages [num_pages,Hkv,page,d] bf16 by table [R,max_pages] int32
+    -> (O [R,H,d] bf16, lse [R,H] f32 or None). H is a multiple of Hkv."""
+    R, H, d = q.shape
+    dev = q.device
+    pq = _arg(q, "q", torch.bfloat16, None, dev)
+    kp, vp = _pool(k_pages, v_pages, dev)
+    num_pages, Hkv, page, dp = k_pages.shape
+    if dp != d:
+        raise ValueError(f"q has heads of {d}, the pages of {dp}")
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError(f"table must be [{R},max_pages]")
+    pt = _arg(table, "table", torch.int32, None, dev)
+    pl = _arg(lens, "lens", torch.int32, (R,), dev)
+    ps = _arg(status, "status", torch.int32, None, dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _guard(q, stream):
+        if ws is None:
+            ws = paged_attn_workspace(R, H, Hkv, d, dev)
+        if out is None:
+            out = torch.empty((R, H, d), dtype=torch.bfloat16, device=dev)
+        if not want_lse:
+            lse = None
+        elif lse is None:
+            lse = torch.empty((R, H), dtype=torch.float32, device=dev)
+        _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages,
+                                    table.shape[1], float(scale),
+                                    _arg(out, "out", torch.bfloat16, (R, H, d), dev),
+                                    _arg(lse, "lse", torch.float32, (R, H), dev),
+                                    _arg(ws, "ws", torch.uint8, None, dev), ws.numel(), ps,
+                                    _stream()), "velox_paged_attn")
+    return out, lse

@@ -66,6 +66,7 @@ extern "C" {
 /* status-word bits */
 #define VELOX_STATUS_BAD_INDEX 1
 #define VELOX_STATUS_TIMEOUT 2
+#define VELOX_STATUS_NO_SPACE 4 /* velox_paged_plan / velox_paged_release: no room; nothing changed */
 
 /* element types */
 #define VELOX_BF16 0
@@ -312,6 +313,199 @@ VELOX_API int velox_depth_multiwarp_noalloc(const float* past_depth,
  * Errors: VELOX_EINVAL for NULL pointers.
  */
 VELOX_API int velox_cast_bf16(const float* x, uint16_t* y, size_t n, void* stream);
+
+/*
+ * ---- Tokens: rotary positions, and a paged cache read by one new token -----
+ *
+ * A chunked world model also handles single tokens (an action, a state, a
+ * caption token per rollout) and several rollouts of different lengths at once.
+ * These calls are the block-sparse path's counterpart for them: rotary positions
+ * of Q and K, a KV cache in pages that many requests share, and the attention of
+ * one new token per request over its own pages.
+ *
+ * The paged cache of one layer is k_pages / v_pages [num_pages][Hkv][page][d]
+ * bf16 (a page holds the heads of `page` consecutive tokens of one request, head by
+ * head, as the block-sparse path's cache holds a whole history). Request r's
+ * token t lies in page table[r][t / page], row t % page; table is [R][max_pages]
+ * int32, and entries behind a request's pages are neither read nor written. A token's
+ * slot is page_id * page + row. Free pages are a stack: the first *free_count
+ * entries of free_list [num_pages], taken from and returned to its end.
+ */
+
+/* pair layouts of velox_rope_t */
+#define VELOX_ROPE_HALF 0        /* pair i = elements (i, i + rot/2) */
+#define VELOX_ROPE_INTERLEAVED 1 /* pair i = elements (2i, 2i + 1) */
+
+/* frequency scalings of velox_rope_freqs */
+#define VELOX_ROPE_PLAIN 0  /* f_i = base^(-2i/rot) */
+#define VELOX_ROPE_LINEAR 1 /* f_i / factor */
+#define VELOX_ROPE_BASE 2   /* base * factor^(rot/(rot-2)) in place of base */
+#define VELOX_ROPE_BANDS 3  /* by wavelength, see velox_rope_freqs */
+
+/* A rotation, a HOST struct that the call reads before it returns.
+ * Element pair i (of rot/2) of a token is turned by the angle
+ * t = pos[axis(i)] * freqs[i]:  (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t),
+ * or by -t when `inverse` is set (the rotation's transpose, so also its gradient).
+ * The first sections[0] pairs take their position from axis 0, the next
+ * sections[1] from axis 1, and so on: one axis for running text or action tokens,
+ * frame, row and column for the tokens of a chunk. Elements from rot on pass
+ * unchanged. Angles are formed in float64, whatever the position; the rotation
+ * runs in float32 and is rounded once. */
+typedef struct velox_rope_t {
+    const double* freqs; /* DEVICE, [rot/2] radians per position */
+    int rot;             /* rotated elements of a head: even, 0 <= rot <= d */
+    int style;           /* VELOX_ROPE_HALF or VELOX_ROPE_INTERLEAVED */
+    int axes;            /* 1 to 3 */
+    int sections[3];     /* pairs of each axis, >= 0; the first `axes` sum to rot/2 */
+    float mscale;
+    int inverse;
+} velox_rope_t;
+
+/*
+ * The frequencies of `rot` rotated elements (of one axis), for velox_rope_t.
+ *   freqs  HOST, [rot/2] float64 output; mscale  HOST, 1 float output, or NULL
+ * kind VELOX_ROPE_BANDS (contexts `factor` times the original one of orig_len
+ * positions): a pair that turns at least beta_fast times over orig_len positions
+ * keeps f_i, one that turns at most beta_slow times gets f_i / factor, and
+ * in between the two are mixed linearly in the pair's index, from floor of the
+ * (real) index with beta_fast turns to ceil of the one with beta_slow, both held
+ * within [0, rot - 1]; *mscale = 0.1 ln(factor) + 1. Every other kind gives
+ * *mscale = 1. orig_len and the betas are read for VELOX_ROPE_BANDS alone.
+ * Runs on the host and launches nothing.
+ * Errors: VELOX_EINVAL for odd or non-positive rot, base <= 1, factor < 1, NULL
+ * freqs, VELOX_ROPE_BASE with rot = 2, for VELOX_ROPE_BANDS orig_len < 1 or
+ * not beta_fast > beta_slow > 0, and for values that are not finite;
+ * VELOX_EUNSUPPORTED for an unknown kind.
+ */
+VELOX_API int velox_rope_freqs(int rot, double base, int kind, double factor, int orig_len,
+                               double beta_fast, double beta_slow, double* freqs, float* mscale);
+
+/*
+ * Rotary positions of a tensor.
+ *   x, y  [B][H][N][d], dtype VELOX_BF16 or VELOX_F32; y may be x (with x's strides)
+ *   xs, ys  HOST, elements between batches, heads and tokens of x and y (the
+ *         innermost dimension is dense); 0 is allowed in xs alone
+ *   pos   int32; token n of batch b has position
+ *         pos[a * pos_axis_stride + b * pos_batch_stride + n] on axis a
+ * Any alignment is taken; rows whose pointers, strides, rot and d allow 16-byte
+ * accesses are faster.
+ * Errors: VELOX_EINVAL for non-positive sizes, B*N or H >= 2^31, d > 4096,
+ * negative strides (or 0 in ys along a dimension longer than 1), an inconsistent
+ * velox_rope_t (NULL freqs with rot > 0, odd rot or rot > d, axes outside 1..3,
+ * sections that do not sum to rot/2, mscale not finite), pointers not aligned to
+ * their element, or NULL x, y, rope, xs, ys (or pos with rot > 0);
+ * VELOX_EUNSUPPORTED for an unknown dtype or style.
+ */
+VELOX_API int velox_rope(const void* x, int dtype, int B, int H, int N, int d, const int64_t* xs,
+                         const int32_t* pos, int64_t pos_axis_stride, int64_t pos_batch_stride,
+                         const velox_rope_t* rope, void* y, const int64_t* ys, void* stream);
+
+/*
+ * Block tables and slot map of a step, from the requests' lengths.
+ *   add   [R] int32     new tokens of each request (0: none)
+ *   lens  [R] int32     tokens already cached
+ *   table [R][max_pages] int32   the new pages are entered behind the old ones
+ *   free_list [num_pages], free_count [1] int32   the free pages (a stack)
+ *   lens_out [R], free_count_out [1] int32 outputs; may be lens and free_count
+ *   cu    [R + 1] int32 output: request r's new tokens are cu[r] .. cu[r+1] - 1
+ *   slots, pos, req [n_cap] int32 outputs: slot, position in its request and
+ *         request of each new token, -1 from token cu[R] on; pos and req may be
+ *         NULL, and slots where n_cap = 0
+ * Request r gets ceil((lens+add)/page) - ceil(lens/page) pages, requests in
+ * order, each from the end of the stack. free_list itself is not changed, so a step
+ * whose outputs are not its inputs may be planned again. Nothing is read back:
+ * the call can be captured and replayed.
+ * A plan that does not fit (more pages than are free, more tokens than n_cap, a
+ * request beyond max_pages pages) changes nothing: lens and free_count are
+ * handed on, cu is 0, every slot, pos and req is -1, and VELOX_STATUS_NO_SPACE
+ * is set. The same with VELOX_STATUS_BAD_INDEX for a negative add, lens outside
+ * [0, max_pages * page] or free_count outside [0, num_pages]. A token whose
+ * page id in table or free_list is outside [0, num_pages) gets slot -1 and sets
+ * VELOX_STATUS_BAD_INDEX.
+ * Errors: VELOX_EINVAL for R outside [1, 8192], n_cap < 0, page, max_pages or
+ * num_pages < 1, max_pages * page or num_pages * page >= 2^31, or NULL
+ * pointers; VELOX_EUNSUPPORTED for page not in {16, 32, 64, 128}.
+ */
+VELOX_API int velox_paged_plan(const int32_t* add, const int32_t* lens, int32_t* table,
+                               const int32_t* free_list, const int32_t* free_count, int R,
+                               int max_pages, int page, int num_pages, int n_cap,
+                               int32_t* lens_out, int32_t* free_count_out, int32_t* cu,
+                               int32_t* slots, int32_t* pos, int32_t* req, int32_t* status,
+                               void* stream);
+
+/*
+ * Gives the pages of finished requests back.
+ *   done [R] int32: non-zero where request r ends. Its pages are pushed on the
+ *   stack (requests in order, pages in order) and its length becomes 0; the
+ *   table keeps its entries, which nothing reads any more.
+ * Other arguments as velox_paged_plan. When more than num_pages pages would be
+ * free (a page given back twice) nothing changes and VELOX_STATUS_NO_SPACE is
+ * set; lens outside [0, max_pages * page] or free_count outside [0, num_pages]:
+ * nothing changes, VELOX_STATUS_BAD_INDEX. Errors as velox_paged_plan.
+ */
+VELOX_API int velox_paged_release(const int32_t* done, const int32_t* lens, const int32_t* table,
+                                  int32_t* free_list, const int32_t* free_count, int R,
+                                  int max_pages, int page, int num_pages, int32_t* lens_out,
+                                  int32_t* free_count_out, int32_t* status, void* stream);
+
+/*
+ * Writes N new tokens into one layer's pages, rotated on the way.
+ *   q [N][H][d] (or NULL), k, v [N][Hkv][d]  dtype VELOX_BF16 or VELOX_F32
+ *   qs, ks, vs  HOST, elements between tokens and between heads (slices of a fused
+ *         projection, or [H][N][d] tensors; the innermost dimension is dense)
+ *   slots [N] int32     slot of each token; negative: the token is padding, its k
+ *         and v are not written. No slot may be given twice
+ *   pos   int32, axis a of token n at pos[a * pos_axis_stride + n]
+ *   rope  rotation of q and k, or NULL (none: pos is not read)
+ *   q_out [N][H][d] bf16 output (dense; NULL without q): every row is written
+ *   k_pages, v_pages [num_pages][Hkv][page][d] bf16; other rows stay as they are
+ * Everything is rounded to bf16 once, after the rotation. A slot of
+ * num_pages * page or more is skipped and sets VELOX_STATUS_BAD_INDEX.
+ * Errors: VELOX_EINVAL for non-positive sizes, N, H or Hkv >= 2^31,
+ * num_pages * page >= 2^31, negative strides, an inconsistent rope (see
+ * velox_rope), pages or q_out not 16-byte aligned, inputs not aligned to their
+ * element, NULL pointers, q without q_out or the reverse; VELOX_EUNSUPPORTED for
+ * page not in {16, 32, 64, 128}, d not in {64, 128}, an unknown dtype or style.
+ */
+VELOX_API int velox_paged_append(const void* q, const void* k, const void* v, int dtype, int N,
+                                 int H, int Hkv, int d, const int64_t* qs, const int64_t* ks,
+                                 const int64_t* vs, const int32_t* slots, const int32_t* pos,
+                                 int64_t pos_axis_stride, const velox_rope_t* rope, void* q_out,
+                                 void* k_pages, void* v_pages, int page, int num_pages,
+                                 int32_t* status, void* stream);
+
+/* Bytes of scratch velox_paged_attn needs for these sizes (0 on bad sizes). */
+VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
+
+/*
+ * Attention of one new token per request over its pages.
+ *   q [R][H][d] bf16 (the layout [B][H][1][d] of the block-sparse path);
+ *   k_pages, v_pages [num_pages][Hkv][page][d] bf16, H a multiple of Hkv: query
+ *   head h reads key head h / (H / Hkv)
+ *   table [R][max_pages], lens [R] int32: request r attends to its first lens[r]
+ *   tokens (its new token among them, once appended)
+ *   o [R][H][d] bf16 output; lse [R][H] float32 output (natural log of the
+ *   softmax denominator of the scaled scores) or NULL
+ *   ws  scratch of velox_paged_attn_workspace_size bytes (256-B aligned)
+ * A request of length 0 gets zeros, with lse = -inf. What lies in a page behind the
+ * last token may be anything, NaN too. Scores and softmax statistics are
+ * float32; probabilities enter the tensor-core product as the sum of two bf16.
+ * The history of every (request, key head) is split evenly over the GPU and
+ * joined in a fixed order: results do not change from call to call.
+ * Page ids outside [0, num_pages) are replaced by page 0 and lens outside
+ * [0, max_pages * page] by the nearer bound; both set VELOX_STATUS_BAD_INDEX.
+ * An expired internal wait sets VELOX_STATUS_TIMEOUT (outputs then undefined).
+ * Errors: VELOX_EINVAL for R < 1 or R > 65535, H < 1, H not a multiple of Hkv,
+ * scale not positive and finite, max_pages or num_pages < 1, max_pages * page or
+ * num_pages * Hkv * page >= 2^31, R * H >= 2^31, ws_bytes too small, NULL or
+ * misaligned (16 B; ws 256 B) pointers; VELOX_EUNSUPPORTED for page not in
+ * {16, 32, 64, 128} or d not in {64, 128}.
+ */
+VELOX_API int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages,
+                               const int32_t* table, const int32_t* lens, int R, int H, int Hkv,
+                               int d, int page, int num_pages, int max_pages, float scale,
+                               void* o, float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                               void* stream);
 
 /*
  * Measurement helper, not a step of the method: blocks x threads threads each
