@@ -12,16 +12,16 @@
 // suit the few query heads (a 128-row tile would be padding), and everything
 // else serves the stream of loads:
 //   - The history is cut in units of 16 tokens (K and V of one key head: 8 KB at
-//     d = 128). Units of all (request, key head, tile of query heads) rows are
-//     numbered in order, and every CTA takes an equal, contiguous share, whatever
-//     the lengths are; no length is read by the host. A CTA's share covers the
-//     end of one row, whole rows, and the beginning of another. Whole rows are
-//     finished here, the others leave (m, l, o) in the workspace, two at most
-//     per CTA, and a second kernel joins them.
-//   - Within a CTA, units go to the warps in turn. A warp runs alone: it
-//     fetches its units by TMA into its own ring of shared memory (128-byte
-//     swizzle), several units ahead and across row ends, and needs no other warp
-//     until the row ends, where the warps' (m, l, o) meet in shared memory.
+//     d = 128). The units of all (request, key head, tile of query heads) rows are
+//     numbered in order, with ROW_COST empty units behind each row for what a
+//     row costs beyond its units, and every warp takes an equal, contiguous share,
+//     whatever the lengths are; no length is read by the host. Rows that lie
+//     inside a share, the many short ones, are finished by their warp alone.
+//   - A warp fetches its units by TMA into its own ring of shared memory (128-byte
+//     swizzle), several units ahead and across row ends, and waits for no other
+//     warp until its share is done. Then the CTA joins the parts of rows that its
+//     warps share, through shared memory; what reaches beyond the CTA (two rows
+//     at most) goes as (m, l, o) to the workspace, and a second kernel joins that.
 //   - S = Q K^T has the query heads in rows 0-7 (and heads 8-15 in rows 8-15, when
 //     more than 8 share a key head). P is split into two bf16, P = hi + lo, with
 //     hi in rows 0-7 and lo in rows 8-15 of one product with V: the rows that 8
@@ -45,9 +45,9 @@ constexpr int UNIT = 16;       // tokens per unit: the smallest page
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most (two per SM)
-// units per CTA at least: a share of fewer would leave warps without work and cost more
-// joining than it saves
-constexpr int MIN_SHARE = 2 * NW;
+constexpr int ROW_COST = 1;    // empty units that a row counts for
+// units per warp at least: fewer would cost more joining than they save
+constexpr int MIN_SHARE = 2;
 
 template <int D, int MT>
 struct Cfg {
@@ -55,46 +55,56 @@ struct Cfg {
     static constexpr int HALF = UNIT * 128;        // 16 tokens x 64 columns
     static constexpr int TILE = UNIT * D * 2;      // K or V of a unit
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int ST = D == 128 ? 3 : 6;    // ring depth per warp
-    static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][8][D]
-    static constexpr int OFF_M = OFF_O + NW * 8 * D * 4;    // float [NW][HEADS]
-    static constexpr int OFF_L = OFF_M + NW * HEADS * 4;    // float [NW][HEADS]
-    static constexpr int OFF_BAR = OFF_L + NW * HEADS * 4;  // uint64 [NW][ST]
-    static constexpr int OFF_SH = OFF_BAR + NW * ST * 8;    // int64 [NW + 4]
-    static constexpr int OFF_ABORT = OFF_SH + (NW + 4) * 8;
+    // ring depth per warp: what two CTAs per SM have room for, 96 KB (64 KB with two
+    // tiles of parts) in flight
+    static constexpr int ST = (D == 128 ? 3 : 6) - (MT == 2 ? (D == 128 ? 1 : 2) : 0);
+    static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][HEADS][D]: a warp's first row
+    static constexpr int OFF_M = OFF_O + NW * HEADS * D * 4;   // float [2 NW][HEADS]
+    static constexpr int OFF_L = OFF_M + 2 * NW * HEADS * 4;   // float [2 NW][HEADS]
+    static constexpr int OFF_SH = OFF_L + 2 * NW * HEADS * 4;  // int64 [NW][6]
+    static constexpr int OFF_BAR = OFF_SH + NW * 6 * 8;        // uint64 [NW][ST]
+    static constexpr int OFF_ENT = OFF_BAR + NW * ST * 8;      // int [2 NW][4]: the parts
+    static constexpr int OFF_ABORT = OFF_ENT + 2 * NW * 16;
     static constexpr int SMEM = OFF_ABORT + 8;
+    static_assert(ST * STAGE >= HEADS * D * 4, "a warp's last row takes its ring's place");
     static constexpr int PART = HEADS * (D + 2);   // floats of a partial result: o, m, l
 };
 
 __device__ __forceinline__ int clamp_len(int n, int cap) { return min(max(n, 0), cap); }
 __device__ __forceinline__ int units_of(int n) { return (n + UNIT - 1) / UNIT; }
 
-// Where the work lies: total units, and the row that holds a given unit.
-struct Place {
-    long long total;
-    int grid;       // CTAs that take a share
-    int r, row, u;  // request, row in it (key head x head tile), unit in the row
+// A row: one key head (and tile of its query heads) of one request. Its real units
+// are base .. base + units - 1 in the numbering of all, ROW_COST empty ones follow.
+struct Row {
+    long long base;
+    int r, row;     // request, row in it
     int n, units;   // tokens and units of the request
-    long long base; // first unit of the row
+};
+struct Work {
+    long long total;  // units, the empty ones included
+    int grid;         // CTAs that take a share
 };
 
-__device__ __forceinline__ long long share(long long total, int grid, int c) {
-    return total * c / grid;
-}
+// where share c of n begins
+__device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
 
-// Every thread of the CTA calls it. Unit number of share `c` -> place (c = grid:
-// only total and grid are set). sh: at least NT + 8 long longs.
-__device__ __forceinline__ void locate(const PagedAttnArgs& a, int c, Place& p, long long* sh,
-                                       bool report) {
+__device__ __forceinline__ int weight(int units) { return units > 0 ? units + ROW_COST : 0; }
+
+// Every thread of the CTA calls it. Counts the work, and finds the rows in which `count`
+// shares begin, from the first-th of grid * per on: sh[6 w] onwards gets share
+// w's row. sh: 6 long longs per share, NW of them at least. The caller lets the CTA
+// meet before it reads sh.
+__device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, int count, int per,
+                                       long long* sh, bool report) {
     const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
-    const int per = (a.R + NT - 1) / NT;
-    const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
+    const int each = (a.R + NT - 1) / NT;
+    const int r0 = min(a.R, static_cast<int>(threadIdx.x) * each), r1 = min(a.R, r0 + each);
     long long mine = 0;
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r];
         bad |= n < 0 || n > cap;
-        mine += units_of(clamp_len(n, cap));
+        mine += weight(units_of(clamp_len(n, cap)));
     }
     if (report && bad && a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
     long long x = mine;
@@ -106,54 +116,58 @@ __device__ __forceinline__ void locate(const PagedAttnArgs& a, int c, Place& p, 
     }
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    long long before = 0, total = 0;
+    long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         if (w < warp) before += sh[w];
-        total += sh[w];
+        all += sh[w];
     }
-    long long first = before + x - mine;  // units of the requests before r0 (one row each)
-    p.total = total * rows;
-    const long long most = (p.total + MIN_SHARE - 1) / MIN_SHARE;
-    p.grid = static_cast<int>(min(static_cast<long long>(a.grid), max(most, 1ll)));
-    if (c < p.grid && p.total > 0) {
-        const long long s = share(p.total, p.grid, c);
-        if (s >= first * rows && s < (first + mine) * rows) {
-            int r = r0;
-            for (; r < r1; ++r) {
-                const int un = units_of(clamp_len(a.lens[r], cap));
-                if (s < (first + un) * rows) break;
-                first += un;
-            }
-            const int n = clamp_len(a.lens[r], cap), un = units_of(n);
-            const long long in = s - first * rows;
-            const int row = static_cast<int>(in / un);
-            sh[NW] = r;
-            sh[NW + 1] = row;
-            sh[NW + 2] = n;
-            sh[NW + 3] = s - (in - static_cast<long long>(row) * un);
+    __syncthreads();
+    Work k;
+    k.total = all * rows;
+    const long long most = (k.total + NW * MIN_SHARE - 1) / (NW * MIN_SHARE);
+    k.grid = static_cast<int>(min(static_cast<long long>(a.grid), max(most, 1ll)));
+    const long long from = (before + x - mine) * rows, to = from + mine * rows;
+    for (int w = 0; w < count; ++w) {
+        if (first_share + w >= k.grid * per) break;
+        const long long s = share(k.total, k.grid * per, first_share + w);
+        if (s < from || s >= to) continue;
+        long long at = from;
+        int r = r0, un = 0, n = 0;
+        for (; r < r1; ++r) {
+            n = clamp_len(a.lens[r], cap);
+            un = units_of(n);
+            const long long next = at + static_cast<long long>(weight(un)) * rows;
+            if (s < next) break;
+            at = next;
         }
-        __syncthreads();
-        p.r = static_cast<int>(sh[NW]);
-        p.row = static_cast<int>(sh[NW + 1]);
-        p.n = static_cast<int>(sh[NW + 2]);
-        p.units = units_of(p.n);
-        p.base = sh[NW + 3];
-        p.u = static_cast<int>(s - p.base);
+        const int row = static_cast<int>((s - at) / weight(un));
+        sh[6 * w] = at + static_cast<long long>(row) * weight(un);
+        sh[6 * w + 1] = r;
+        sh[6 * w + 2] = row;
+        sh[6 * w + 3] = n;
     }
+    return k;
 }
 
-// the next row that has units, after the one at p (which exists: the caller knows
-// that units are left)
-__device__ __forceinline__ void next_row(const PagedAttnArgs& a, Place& p) {
-    const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
-    p.base += p.units;
-    p.u = 0;
-    if (++p.row < rows) return;
+__device__ __forceinline__ Row located(const long long* sh) {
+    Row p;
+    p.base = sh[0];
+    p.r = static_cast<int>(sh[1]);
+    p.row = static_cast<int>(sh[2]);
+    p.n = static_cast<int>(sh[3]);
+    p.units = units_of(p.n);
+    return p;
+}
+
+// the next row that has units (the caller knows that there is one)
+__device__ __forceinline__ void next_row(const PagedAttnArgs& a, Row& p) {
+    p.base += weight(p.units);
+    if (++p.row < a.Hkv * a.head_tiles) return;
     p.row = 0;
     do {
         ++p.r;
-        p.n = p.r < a.R ? clamp_len(a.lens[p.r], cap) : UNIT;
+        p.n = p.r < a.R ? clamp_len(a.lens[p.r], a.max_pages * a.page) : UNIT;
     } while (p.n == 0);
     p.units = units_of(p.n);
 }
@@ -189,6 +203,21 @@ __device__ __forceinline__ uint32_t tile_at(int row, int c) {
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 
+// where entry e's unnormalised output lies: a warp's part 0 in its own place, its part
+// 1 in its ring
+template <int D, int MT>
+__device__ __forceinline__ float* part_o(uint8_t* smem, int e) {
+    using C = Cfg<D, MT>;
+    const int warp = e >> 1;
+    return reinterpret_cast<float*>((e & 1) ? smem + warp * C::ST * C::STAGE
+                                            : smem + C::OFF_O + warp * C::HEADS * D * 4);
+}
+
+// natural log of the softmax denominator from the base-2 maximum and sum
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(NT, 2)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -204,7 +233,7 @@ __global__ void __launch_bounds__(NT, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = sbase + warp * C::ST * C::STAGE;
     const uint32_t bars = sbase + C::OFF_BAR + warp * C::ST * 8;
-    const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
+    const int cap = a.max_pages * a.page;
 
     // lets the joining kernel's CTAs settle on the SMs; they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;");
@@ -229,35 +258,37 @@ __global__ void __launch_bounds__(NT, 2)
                 a.lse[static_cast<long long>(r) * a.H + h] = -INFINITY;
     }
 
-    Place p;
     const int cta = blockIdx.x;
-    locate(a, cta, p, sh, cta == 0);
-    __syncthreads();  // barriers initialised
-    if (cta >= p.grid || p.total == 0) return;
-    const long long s0 = share(p.total, p.grid, cta), s1 = share(p.total, p.grid, cta + 1);
-    if (s0 >= s1) return;
+    const Work work = locate(a, cta * NW, NW, NW, sh, cta == 0);
+    __syncthreads();  // rows found, barriers initialised
+    if (cta >= work.grid || work.total == 0) return;
+    // this warp's share: units g0 .. g1 - 1
+    const long long g0 = share(work.total, work.grid * NW, cta * NW + warp);
+    const long long g1 = share(work.total, work.grid * NW, cta * NW + warp + 1);
+    Row p = located(sh + 6 * warp);
 
-    // ---- this warp's loads: units s0 + warp, + NW, ... of the CTA's share
-    Place f = p;                   // row of the next unit to fetch
-    long long fg = s0 + warp;      // its number
-    int page_id = 0, page_row = 0; // its page, looked up one unit ahead
-    auto find = [&]() {            // moves f to unit fg and looks its page up
-        if (fg >= s1) return;
-        while (fg >= f.base + f.units) next_row(a, f);
+    // ---- loads, ahead of the products and across rows
+    Row f = p;
+    long long fg = g0;              // next unit to fetch
+    int page_id = 0, page_row = 0;  // its page, looked up one unit ahead
+    auto find = [&]() {
+        while (fg < g1 && fg >= f.base + f.units) {  // the row's real units are over
+            fg = f.base + weight(f.units);
+            if (fg < g1) next_row(a, f);
+        }
+        if (fg >= g1) return;
         const int tok = static_cast<int>(fg - f.base) * UNIT;
         page_row = tok & (a.page - 1);
-        page_id = a.table[static_cast<long long>(f.r) * a.max_pages + tok / a.page];
+        page_id = a.table[static_cast<long long>(f.r) * a.max_pages + (tok >> a.page_shift)];
     };
-    int f_head = 0;
-    auto fetch = [&](int slot) {  // lane 0 fetches unit fg into `slot`
+    auto fetch = [&](int slot) {
         if (lane == 0) {
             int id = page_id;
             if (id < 0 || id >= a.num_pages) {
                 if (a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
                 id = 0;
             }
-            f_head = f.row / a.head_tiles;
-            const int y = (id * a.Hkv + f_head) * a.page + page_row;
+            const int y = (id * a.Hkv + f.row / a.head_tiles) * a.page + page_row;
             const uint32_t bar = bars + 8 * slot, dst = ring + slot * C::STAGE;
             mbar_arrive_expect_tx(bar, C::STAGE);
 #pragma unroll
@@ -266,41 +297,42 @@ __global__ void __launch_bounds__(NT, 2)
             for (int h = 0; h < D / 64; ++h)
                 tma_load_2d(dst + C::TILE + h * C::HALF, &tmV, bar, 64 * h, y);
         }
-        fg += NW;
+        ++fg;
         find();
     };
     find();
-    int issued = 0;  // units fetched so far, modulo nothing: counts up
+    int ahead = 0;  // units fetched and not yet used
     for (int s = 0; s < C::ST; ++s)
-        if (fg < s1) {
+        if (fg < g1) {
             fetch(s);
-            ++issued;
+            ++ahead;
         }
 
     const int g = lane >> 2, t = lane & 3;
-    int done = 0, slot = 0;
+    int* ent = reinterpret_cast<int*>(smem + C::OFF_ENT) + 8 * warp;  // this warp's two parts
+    if (lane < 2) ent[4 * lane] = -1;  // none yet
+    int slot = 0;
     uint32_t parity = 0;
     bool ok = true;
-    long long cg = s0 + warp;  // this warp's next unit
-    for (long long at = s0; at < s1;) {
-        const long long row_end = min(p.base + p.units, s1);
-        const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
-        const int head0 = hk * a.group + ht * a.tile_heads;
-        const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
-        const long long q_row = static_cast<long long>(p.r) * a.H + head0;
+    while (true) {
+        // units of this row in the share
+        const int u0 = static_cast<int>(max(g0 - p.base, 0ll));
+        const int u1 = static_cast<int>(min(g1 - p.base, static_cast<long long>(p.units)));
+        if (u0 < u1) {
+            const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
+            const int head0 = hk * a.group + ht * a.tile_heads;
+            const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
+            const long long q_row = static_cast<long long>(p.r) * a.H + head0;
 
-        float o[MT][D / 8][4];
-        float m[MT], l[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            m[i] = -INFINITY, l[i] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
-        }
-        if (cg < row_end) {
+            float o[MT][D / 8][4];
+            float m[MT], l[MT];
             uint32_t q[MT][D / 16][2];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
+                m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.0f;
                 const bool have = 8 * i + g < heads;
                 const uint32_t* src =
                     reinterpret_cast<const uint32_t*>(a.q + (q_row + (have ? 8 * i + g : 0)) * D) + t;
@@ -310,12 +342,12 @@ __global__ void __launch_bounds__(NT, 2)
                     q[i][k][1] = have ? src[8 * k + 4] : 0u;
                 }
             }
-            for (; cg < row_end; cg += NW) {
-                ok = ok && mbar_wait(bars + 8 * slot, parity, abort_flag, a.wait_ns);
+            for (int u = u0; u < u1; ++u) {
+                ok = mbar_wait(bars + 8 * slot, parity, abort_flag, a.wait_ns);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 const uint32_t kt = ring + slot * C::STAGE, vt = kt + C::TILE;
-                const int valid = p.n - static_cast<int>(cg - p.base) * UNIT;  // tokens left
+                const int valid = p.n - u * UNIT;  // tokens left
                 if (valid < UNIT) {
                     // values behind the last token may be anything: their weight is 0, but
                     // 0 * NaN is not
@@ -392,103 +424,147 @@ __global__ void __launch_bounds__(NT, 2)
                     }
                 }
                 __syncwarp();  // every lane has read the slot
-                ++done;
-                if (fg < s1) {
+                --ahead;
+                if (fg < g1) {
                     fetch(slot);
-                    ++issued;
+                    ++ahead;
                 }
                 if (++slot == C::ST) slot = 0, parity ^= 1;
             }
-        }
-        // ---- the row (or this CTA's part of it) is done: join the warps
-        float* sm_o = reinterpret_cast<float*>(smem + C::OFF_O);
-        float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
-        float* sm_l = reinterpret_cast<float*>(smem + C::OFF_L);
-        const bool whole = at == p.base && row_end == p.base + p.units;
-        float* part = a.part + static_cast<long long>(2 * cta + (at == s0 ? 0 : 1)) * C::PART;
+            if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            l[i] += __shfl_xor_sync(~0u, l[i], 1);
-            l[i] += __shfl_xor_sync(~0u, l[i], 2);
-            if (t == 0) sm_m[warp * C::HEADS + 8 * i + g] = m[i], sm_l[warp * C::HEADS + 8 * i + g] = l[i];
-            if (8 * i + g < heads) {
+            for (int i = 0; i < MT; ++i) {
+                l[i] += __shfl_xor_sync(~0u, l[i], 1);
+                l[i] += __shfl_xor_sync(~0u, l[i], 2);
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
-                    float v0 = o[i][j][0], v1 = o[i][j][1];
-                    if (isfinite(o[i][j][2])) v0 += o[i][j][2];
-                    if (isfinite(o[i][j][3])) v1 += o[i][j][3];
-                    *reinterpret_cast<float2*>(sm_o + (warp * 8 + g) * D + 8 * j + 2 * t) =
-                        make_float2(v0, v1);
+                    if (isfinite(o[i][j][2])) o[i][j][0] += o[i][j][2];
+                    if (isfinite(o[i][j][3])) o[i][j][1] += o[i][j][3];
                 }
             }
-            __syncthreads();
-            for (int e = threadIdx.x; e < 8 * D; e += NT) {
-                const int h = e / D, col = e % D, hh = 8 * i + h;
-                if (hh >= heads) break;
-                float top = sm_m[hh];
+            const bool begins = u0 == 0, ends = u1 == p.units;
+            if (begins && ends) {
 #pragma unroll
-                for (int w = 1; w < NW; ++w) top = fmaxf(top, sm_m[w * C::HEADS + hh]);
-                const float ref = top == -INFINITY ? 0.0f : top;
-                float sum = 0.0f, acc = 0.0f;
+                for (int i = 0; i < MT; ++i)
+                    if (8 * i + g < heads) {
+                        const float inv = 1.0f / l[i];
+                        uint32_t* dst =
+                            reinterpret_cast<uint32_t*>(a.o + (q_row + 8 * i + g) * D) + t;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const float x = ex2_approx(sm_m[w * C::HEADS + hh] - ref);
-                    sum += x * sm_l[w * C::HEADS + hh];
-                    // a warp without units has m = -inf and o = 0
-                    acc += x * sm_o[(w * 8 + h) * D + col];
-                }
-                if (whole) {
-                    a.o[(q_row + hh) * D + col] = __float2bfloat16_rn(acc / sum);
-                    if (a.lse && col == 0)
-                        a.lse[q_row + hh] = (ref + log2f(sum)) * 0.6931471805599453f;
-                } else {
-                    part[hh * D + col] = acc;
-                    if (col == 0) {
-                        part[C::HEADS * D + hh] = top;
-                        part[C::HEADS * D + C::HEADS + hh] = sum;
+                        for (int j = 0; j < D / 8; ++j)
+                            dst[4 * j] = pack_bf16x2(o[i][j][0] * inv, o[i][j][1] * inv);
+                        if (a.lse && t == 0) a.lse[q_row + 8 * i + g] = log_sum(m[i], l[i]);
                     }
+            } else {
+                // part 0: the end of a row that another warp began; part 1: a row that
+                // goes on in the next warp. Part 1 is this warp's last row, so its ring
+                // has no load in flight
+                const int e = 2 * warp + (ends ? 0 : 1);
+                float* sm_o = part_o<D, MT>(smem, e);
+                float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M) + e * C::HEADS;
+                float* sm_l = reinterpret_cast<float*>(smem + C::OFF_L) + e * C::HEADS;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if (t == 0) sm_m[8 * i + g] = m[i], sm_l[8 * i + g] = l[i];
+                    if (8 * i + g < heads)
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j)
+                            *reinterpret_cast<float2*>(sm_o + (8 * i + g) * D + 8 * j + 2 * t) =
+                                make_float2(o[i][j][0], o[i][j][1]);
+                }
+                if (lane == 0) {
+                    int* mine = ent + (ends ? 0 : 4);
+                    mine[1] = p.r;
+                    mine[2] = p.row;
+                    mine[3] = begins;
+                    mine[0] = 1;
                 }
             }
-            __syncthreads();
         }
-        at = row_end;
-        if (at < s1) next_row(a, p);
+        if (p.base + weight(p.units) >= g1) break;
+        next_row(a, p);
     }
     // a wait that ran out: what is still in flight lands before the CTA leaves
     if (!ok) {
         if (lane == 0 && a.status) atomicOr(a.status, VELOX_STATUS_TIMEOUT);
         volatile int never = 0;
-        for (; done < issued; ++done) {
+        for (; ahead > 0; --ahead) {
             if (!mbar_wait(bars + 8 * slot, parity, &never, a.wait_ns)) break;
             if (++slot == C::ST) slot = 0, parity ^= 1;
         }
     }
+
+    // ---- rows that several warps worked on. In the order of the entries, a row's parts
+    // follow one another: parts 1 (it goes on), then a part 0 (it ends) if it ends
+    // in this CTA
+    __syncthreads();
+    const int* ents = reinterpret_cast<const int*>(smem + C::OFF_ENT);
+    const float* sm_m = reinterpret_cast<const float*>(smem + C::OFF_M);
+    const float* sm_l = reinterpret_cast<const float*>(smem + C::OFF_L);
+    for (int e0 = 0; e0 < 2 * NW; ++e0) {
+        if (ents[4 * e0] < 0) continue;
+        int e1 = e0;  // last entry of the row
+        bool ends = (e0 & 1) == 0;
+        for (int e = e0 + 1; e < 2 * NW && !ends; ++e)
+            if (ents[4 * e] >= 0) e1 = e, ends = (e & 1) == 0;
+        const int r = ents[4 * e0 + 1], row = ents[4 * e0 + 2];
+        const bool begins = ents[4 * e0 + 3] != 0;
+        const int hk = row / a.head_tiles, ht = row - hk * a.head_tiles;
+        const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
+        const long long q_row =
+            static_cast<long long>(r) * a.H + hk * a.group + ht * a.tile_heads;
+        float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
+        for (int i = threadIdx.x; i < heads * D; i += NT) {
+            const int h = i / D, col = i % D;
+            float top = -INFINITY;
+            for (int e = e0; e <= e1; ++e)
+                if (ents[4 * e] >= 0) top = fmaxf(top, sm_m[e * C::HEADS + h]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f, acc = 0.0f;
+            for (int e = e0; e <= e1; ++e)
+                if (ents[4 * e] >= 0) {
+                    const float x = ex2_approx(sm_m[e * C::HEADS + h] - ref);
+                    sum += x * sm_l[e * C::HEADS + h];
+                    acc += x * part_o<D, MT>(smem, e)[h * D + col];
+                }
+            if (begins && ends) {
+                a.o[(q_row + h) * D + col] = __float2bfloat16_rn(acc / sum);
+                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top, sum);
+            } else {
+                part[h * D + col] = acc;
+                if (col == 0) {
+                    part[C::HEADS * D + h] = top;
+                    part[C::HEADS * D + C::HEADS + h] = sum;
+                }
+            }
+        }
+        e0 = e1;
+    }
 }
 
-// Joins the parts of the rows that more than one CTA worked on. CTA (c, head):
-// if share c is the first to begin inside a row that an earlier share began, it
-// joins that row's query head. A row's parts are those of consecutive shares; the
-// order of the sums is fixed.
+// Joins the parts of the rows that more than one CTA worked on. CTA (c - 1, head):
+// where share c begins inside a row, and is the first to do so, one query head of
+// that row. The row's parts are those of consecutive shares; the order of the
+// sums is fixed.
 template <int D, int MT>
 __global__ void __launch_bounds__(NT)
     paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
     using C = Cfg<D, MT>;
-    __shared__ long long sh[NW + 4];
+    __shared__ long long sh[6 * NW];
     __shared__ float red_m[NW], red_l[NW], red_o[NW][D];
-    Place p;
     const int c = blockIdx.x + 1, hh = blockIdx.y;
-    locate(a, c, p, sh, false);
+    const Work work = locate(a, c, 1, 1, sh, false);
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c >= p.grid || p.total == 0) return;
-    const long long s = share(p.total, p.grid, c);
-    // a share before this one began the row, and none but that one lies before
-    if (s == p.base || share(p.total, p.grid, c - 1) > p.base) return;
+    if (c >= work.grid || work.total == 0) return;
+    const Row p = located(sh);
+    const long long s = share(work.total, work.grid, c), end = p.base + p.units;
+    if (s <= p.base || s >= end || share(work.total, work.grid, c - 1) > p.base) return;
     const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
     const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
     if (hh >= heads) return;
-    const long long end = p.base + p.units;
     // the last share that begins before the row's end
-    const int last = static_cast<int>((end * p.grid - 1) / p.total);
+    const int last = static_cast<int>((end * work.grid - 1) / work.total);
     const int first = c - 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int PER = D / 32;
@@ -497,8 +573,8 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
     for (int i = first + warp; i <= last; i += NW) {
-        // a share's first row is its part 0
-        const int which = 2 * i + (share(p.total, p.grid, i) >= p.base ? 0 : 1);
+        // part 1 of the share in which the row begins, part 0 of the others
+        const int which = 2 * i + (share(work.total, work.grid, i) <= p.base ? 1 : 0);
         const float* part = a.part + static_cast<long long>(which) * C::PART;
         const float m = part[C::HEADS * D + hh], l = part[C::HEADS * D + C::HEADS + hh];
         float v[PER];
@@ -531,7 +607,7 @@ __global__ void __launch_bounds__(NT)
         const long long row =
             static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads + hh;
         a.o[row * D + threadIdx.x] = __float2bfloat16_rn(o / l);
-        if (a.lse && threadIdx.x == 0) a.lse[row] = (ref + log2f(l)) * 0.6931471805599453f;
+        if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(m, l);
     }
 }
 
@@ -581,6 +657,7 @@ int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnA
     a.group = a.H / a.Hkv;
     a.head_tiles = (a.group + 15) / 16;
     a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
+    for (a.page_shift = 4; (1 << a.page_shift) < a.page; ++a.page_shift) {}
     const bool wide = a.group > 8;
     if (d == 128)
         return wide ? launch<128, 2>(k_pages, v_pages, a, st) : launch<128, 1>(k_pages, v_pages, a, st);

@@ -124,6 +124,7 @@ struct PagedAttnArgs {
     int head_tiles;  // tiles of at most 16 query heads per key head
     int tile_heads;  // query heads per tile
     int grid;        // CTAs that share the work
+    int page_shift;  // log2(page)
     float scale_log2;
     __nv_bfloat16* o;
     float* lse;

@@ -11,8 +11,8 @@ znear, zfar.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -364,66 +364,84 @@ def depth_multiwarp_noalloc(past_depth: torch.Tensor, past_cams: torch.Tensor,
 
 # ---------------------------------------------------------------- tokens: rotary positions, paged cache
 
-_NO_GUARD = contextlib.nullcontext()
+# These calls are short, some only a few microseconds on the GPU, so what the
+# binding does per call counts: an argument is looked at once, small outputs
+# share one allocation, and the raw stream handle is taken without building a
+# Stream object (1.5 to 3 us each on the host of a B200).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_I32, _F32, _BF16, _F64 = torch.int32, torch.float32, torch.bfloat16, torch.float64
 
 
-def _guard(x: torch.Tensor, stream):
-    """Where a call on x runs: x's device, and `stream` if one is given. Outputs
-    and scratch are allocated inside, so that they belong to that stream."""
-    if not x.is_cuda:
+def _elsewhere(x: torch.Tensor, stream):
+    """None where a call on x can run as things stand; else the context to run it
+    in: x's device, and `stream` if one is given. Outputs and scratch are then
+    allocated there too."""
+    index = x.get_device()
+    if index < 0:
         raise ValueError("libvelox takes CUDA tensors")
     if stream is not None:
         if stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
         return torch.cuda.stream(stream)
-    if x.device.index != torch.cuda.current_device():
-        return torch.cuda.device(x.device)
-    return _NO_GUARD
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
+    return None
 
 
-def _arg(t: torch.Tensor | None, name: str, dtype: torch.dtype | None, shape: tuple | None,
-         device: torch.device, dense: bool = True):
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None, index: int,
+         dense: bool = True) -> int:
     """The address of an argument after its type, shape, device and layout have been looked at."""
-    if t is None:
-        return None
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
     if dense and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
+def _int64s(values: tuple):
+    """A host array the library reads; equal values share one."""
+    return (_c_i64 * len(values))(*values)
+
+
 def _rows(t: torch.Tensor, name: str) -> tuple:
     """The strides of a tensor whose innermost dimension is dense, 0 along dimensions of size 1."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
-    return tuple(st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()))
+    return tuple([st if n > 1 else 0 for n, st in zip(shape[:-1], stride)])
 
 
 def _in_dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _BF16:
         return VELOX_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is _F32:
         return VELOX_F32
     raise TypeError(f"{name}: unsupported dtype {t.dtype}")
 
 
-def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse: bool,
-               device: torch.device) -> _Rope:
+@functools.lru_cache(maxsize=256)
+def _sections(style: str, sections: tuple):
     if style not in ROPE_STYLES:
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
-    if freqs.dim() != 1:
-        raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
-    sections = (freqs.shape[0],) if sections is None else tuple(int(s) for s in sections)
     if not 1 <= len(sections) <= 3:
         raise ValueError("one to three position axes")
-    return _Rope(_arg(freqs, "freqs", torch.float64, None, device), 2 * freqs.shape[0],
-                 ROPE_STYLES[style], len(sections),
-                 (_c_int * 3)(*sections), float(mscale), int(bool(inverse)))
+    return ROPE_STYLES[style], len(sections), (_c_int * 3)(*sections)
+
+
+def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse: bool,
+               index: int) -> _Rope:
+    if freqs.dim() != 1:
+        raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
+    n = freqs.shape[0]
+    code, axes, sec = _sections(style, (n,) if sections is None else tuple(sections))
+    return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, mscale,
+                 1 if inverse else 0)
 
 
 def _pos_shape(pos: torch.Tensor, axes: int, N: int, B: int | None) -> tuple:
@@ -454,25 +472,31 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rotary positions of x [B,H,N,d] (bf16 or f32; any strides, the last dimension
     dense) -> the same shape and type. pos int32 [N] (one axis), [axes,N] or
-    [axes,B,N]; freqs [rot/2] float64; sections: pairs of each axis (default: one axis).
-    inverse turns back (which is also the gradient of the forward call); out may
-    be x itself."""
-    B, H, N, d = x.shape
+    [axes,B,N]; freqs [rot/2] float64; sections: pairs of each axis (default: one
+    axis). inverse turns back (which is also the gradient of the forward call); out
+    may be x itself."""
+    B, H, N, d = shape = x.shape
+    index = x.get_device()
     dt = _in_dtype(x, "x")
-    spec = _rope_spec(freqs, style, sections, mscale, inverse, x.device)
-    p = _arg(pos, "pos", torch.int32, _pos_shape(pos, spec.axes, N, B), x.device)
-    batched = pos.dim() == 3
+    spec = _rope_spec(freqs, style, sections, mscale, inverse, index)
+    p = _arg(pos, "pos", _I32, _pos_shape(pos, spec.axes, N, B), index)
     xs = _rows(x, "x")
-    with _guard(x, stream):
-        if out is None:
-            out = torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
-        y = _arg(out, "out", x.dtype, (B, H, N, d), x.device, dense=False)
+    there = _elsewhere(x, stream)
+    if there is not None:
+        with there:
+            return rope(x, pos, freqs, style, sections, mscale, inverse, out)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ys = (H * N * d, N * d, d)
+    else:
+        _arg(out, "out", x.dtype, shape, index, dense=False)
         ys = _rows(out, "out")
-        if y == x.data_ptr() and ys != xs:
+        if out.data_ptr() == x.data_ptr() and ys != xs:
             raise ValueError("out may be x itself, not another view of it")
-        _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, (_c_i64 * 3)(*xs), p,
-                              B * N if batched else N, N if batched else 0,
-                              ctypes.byref(spec), y, (_c_i64 * 3)(*ys), _stream()), "velox_rope")
+    batched = pos.dim() == 3
+    _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, _int64s(xs), p, B * N if batched else N,
+                          N if batched else 0, ctypes.byref(spec), out.data_ptr(), _int64s(ys),
+                          _raw_stream(index)), "velox_rope")
     return out
 
 
@@ -488,18 +512,17 @@ class PagedPlan(NamedTuple):
     free_count: torch.Tensor
 
 
-def _pages_state(lens, table, free_list, free_count):
-    """Checks the state of a paged cache; (R, max_pages, num_pages, device, addresses)."""
-    dev = lens.device
+def _pages_state(lens, table, free_list, free_count, index: int):
+    """Checks the state of a paged cache; (R, max_pages, num_pages, its addresses)."""
     if lens.dim() != 1 or table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("lens [R], table [R,max_pages], free_list [num_pages]")
-    R, i32 = lens.shape[0], torch.int32
-    if table.shape[0] != R:
-        raise ValueError(f"table has {table.shape[0]} rows for {R} requests")
-    ptrs = (_arg(lens, "lens", i32, None, dev), _arg(table, "table", i32, None, dev),
-            _arg(free_list, "free_list", i32, None, dev),
-            _arg(free_count, "free_count", i32, (1,), dev))
-    return R, table.shape[1], free_list.shape[0], dev, ptrs
+    R = lens.shape[0]
+    tr, width = table.shape
+    if tr != R:
+        raise ValueError(f"table has {tr} rows for {R} requests")
+    return (R, width, free_list.shape[0], _arg(lens, "lens", _I32, None, index),
+            _arg(table, "table", _I32, None, index), _arg(free_list, "free_list", _I32, None, index),
+            _arg(free_count, "free_count", _I32, (1,), index))
 
 
 def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_list: torch.Tensor,
@@ -508,23 +531,35 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
     """Pages for add [R] new tokens of requests with lens [R] cached ones: enters
     them in table [R,max_pages] and returns the step's PagedPlan with room for n_cap
     tokens (all int32). `out` gives the outputs' tensors; its lens and
-    free_count may be the inputs, so that a captured step carries its state on."""
-    R, max_pages, num_pages, dev, (pl, pt, pf, pc) = _pages_state(lens, table, free_list, free_count)
-    i32 = torch.int32
-    pa = _arg(add, "add", i32, (R,), dev)
-    ps = _arg(status, "status", i32, None, dev)
-    n_cap = int(n_cap)
+    free_count may be the inputs, so that a captured step carries its state on.
+    Tensors allocated here are views of one buffer."""
+    index = lens.get_device()
+    R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
+    pa = _arg(add, "add", _I32, (R,), index)
+    ps = None if status is None else _arg(status, "status", _I32, None, index)
     if not 0 <= n_cap < 2 ** 31:
         raise ValueError("n_cap must be in [0, 2^31)")
-    with _guard(lens, stream):
-        if out is None:
-            e = lambda n: torch.empty(n, dtype=i32, device=dev)  # noqa: E731
-            out = PagedPlan(e(R + 1), e(n_cap), e(n_cap), e(n_cap), e(R), e(1))
-        o = [_arg(t, name, i32, (size,), dev) for t, name, size in
-             zip(out, PagedPlan._fields, (R + 1, n_cap, n_cap, n_cap, R, 1))]
-        _check(lib.velox_paged_plan(pa, pl, pt, pf, pc, R, max_pages, int(page), num_pages, n_cap,
-                                    o[4], o[5], o[0], o[1], o[2], o[3], ps, _stream()),
-               "velox_paged_plan")
+    there = _elsewhere(lens, stream)
+    if there is not None:
+        with there:
+            return paged_plan(add, lens, table, free_list, free_count, page, n_cap, out, status)
+    if out is None:
+        buf = torch.empty(2 * R + 2 + 3 * n_cap, dtype=_I32, device=lens.device)
+        o = buf.data_ptr()
+        # slots, pos and req first: their rows then start where the buffer's alignment allows
+        os_, op, oq = o, o + 4 * n_cap, o + 8 * n_cap
+        oc = o + 12 * n_cap
+        ol = oc + 4 * (R + 1)
+        of = ol + 4 * R
+        slots, pos, req, cu, lens_out, count = buf.split_with_sizes(
+            (n_cap, n_cap, n_cap, R + 1, R, 1))
+        out = PagedPlan(cu, slots, pos, req, lens_out, count)
+    else:
+        oc, os_, op, oq, ol, of = [
+            _arg(t, name, _I32, (size,), index) for t, name, size in
+            zip(out, PagedPlan._fields, (R + 1, n_cap, n_cap, n_cap, R, 1))]
+    _check(lib.velox_paged_plan(pa, pl, pt, pf, pc, R, width, page, num_pages, n_cap, ol, of, oc,
+                                os_, op, oq, ps, _raw_stream(index)), "velox_paged_plan")
     return out
 
 
@@ -533,28 +568,26 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                   lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
                   status: torch.Tensor | None = None, stream=None):
     """The pages of the requests with done [R] != 0 go back on free_list (in
-    place); returns (lens, free_count) afterwards. The outputs may be the inputs."""
-    R, max_pages, num_pages, dev, (pl, pt, pf, pc) = _pages_state(lens, table, free_list, free_count)
-    i32 = torch.int32
-    pd = _arg(done, "done", i32, (R,), dev)
-    ps = _arg(status, "status", i32, None, dev)
-    with _guard(lens, stream):
-        if lens_out is None:
-            lens_out = torch.empty(R, dtype=i32, device=dev)
-        if free_count_out is None:
-            free_count_out = torch.empty(1, dtype=i32, device=dev)
-        _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, max_pages, int(page), num_pages,
-                                       _arg(lens_out, "lens_out", i32, (R,), dev),
-                                       _arg(free_count_out, "free_count_out", i32, (1,), dev), ps,
-                                       _stream()), "velox_paged_release")
+    place); returns (lens, free_count) afterwards. The outputs may be the inputs;
+    those allocated here are views of one buffer."""
+    index = lens.get_device()
+    R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
+    pd = _arg(done, "done", _I32, (R,), index)
+    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    there = _elsewhere(lens, stream)
+    if there is not None:
+        with there:
+            return paged_release(done, lens, table, free_list, free_count, page, lens_out,
+                                 free_count_out, status)
+    if lens_out is None or free_count_out is None:
+        a, b = torch.empty(R + 1, dtype=_I32, device=lens.device).split_with_sizes((R, 1))
+        lens_out = a if lens_out is None else lens_out
+        free_count_out = b if free_count_out is None else free_count_out
+    _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, page, num_pages,
+                                   _arg(lens_out, "lens_out", _I32, (R,), index),
+                                   _arg(free_count_out, "free_count_out", _I32, (1,), index), ps,
+                                   _raw_stream(index)), "velox_paged_release")
     return lens_out, free_count_out
-
-
-def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, device: torch.device):
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages must be [num_pages,Hkv,page,d]")
-    return (_arg(k_pages, "k_pages", torch.bfloat16, None, device),
-            _arg(v_pages, "v_pages", torch.bfloat16, tuple(k_pages.shape), device))
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
@@ -566,40 +599,49 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     to their slots [N] int32 (negative: padding) of k_pages / v_pages
     [num_pages,Hkv,page,d] bf16, in place. With freqs (see rope) k and q
     [N,H,d] are rotated to pos [axes,N] int32 ([N] for one axis) on the way.
-    Returns q as bf16 [N,H,d], or None without q."""
-    N, Hkv, d = k.shape
-    dev = k.device
+    Returns q as bf16 [N,H,d], or None without q; out may be q itself (bf16 and
+    contiguous)."""
+    N, Hkv, d = shape = k.shape
+    index = k.get_device()
     dt = _in_dtype(k, "k")
-    kp, vp = _pool(k_pages, v_pages, dev)
-    num_pages, hp, page, dp = k_pages.shape
-    if (hp, dp) != (Hkv, d):
+    num_pages, hp, page, dp = pages = k_pages.shape
+    if hp != Hkv or dp != d:
         raise ValueError(f"k has {Hkv} heads of {d}, the pages {hp} of {dp}")
-    pv = _arg(v, "v", k.dtype, (N, Hkv, d), dev, dense=False)
-    psl = _arg(slots, "slots", torch.int32, (N,), dev)
-    ps = _arg(status, "status", torch.int32, None, dev)
-    ks, vs = (_c_i64 * 2)(*_rows(k, "k")), (_c_i64 * 2)(*_rows(v, "v"))
+    kp = _arg(k_pages, "k_pages", _BF16, None, index)
+    vp = _arg(v_pages, "v_pages", _BF16, pages, index)
+    pv = _arg(v, "v", k.dtype, shape, index, dense=False)
+    psl = _arg(slots, "slots", _I32, (N,), index)
+    ps = None if status is None else _arg(status, "status", _I32, None, index)
     spec = pp = None
     if freqs is not None:
-        spec = _rope_spec(freqs, style, sections, mscale, False, dev)
         if pos is None:
             raise ValueError("freqs without pos")
-        pp = _arg(pos, "pos", torch.int32, _pos_shape(pos, spec.axes, N, None), dev)
-    H, pq, qs = 0, None, None
+        spec = _rope_spec(freqs, style, sections, mscale, False, index)
+        pp = _arg(pos, "pos", _I32, _pos_shape(pos, spec.axes, N, None), index)
+        spec = ctypes.byref(spec)
+    H, pq, po, qs = 0, None, None, None
     if q is not None:
         H = q.shape[1]
-        pq = _arg(q, "q", k.dtype, (N, H, d), dev, dense=False)
-        qs = (_c_i64 * 2)(*_rows(q, "q"))
+        pq = _arg(q, "q", k.dtype, (N, H, d), index, dense=False)
+        qs = _int64s(_rows(q, "q"))
     elif out is not None:
         raise ValueError("out without q")
-    with _guard(k, stream):
-        if q is not None and out is None:
-            out = torch.empty((N, H, d), dtype=torch.bfloat16, device=dev)
-        po = _arg(out, "out", torch.bfloat16, (N, H, d), dev)
-        if po is not None and po == pq and (q.dtype != torch.bfloat16 or not q.is_contiguous()):
+    ks, vs = _int64s(_rows(k, "k")), _int64s(_rows(v, "v"))
+    there = _elsewhere(k, stream)
+    if there is not None:
+        with there:
+            return paged_append(k, v, slots, k_pages, v_pages, q, pos, freqs, style, sections,
+                                mscale, out, status)
+    if out is not None:
+        po = _arg(out, "out", _BF16, (N, H, d), index)
+        if po == pq and (dt != VELOX_BF16 or not q.is_contiguous()):
             raise ValueError("out may be q itself only where q is contiguous bf16")
-        _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
-                                      ctypes.byref(spec) if spec is not None else None, po, kp, vp,
-                                      page, num_pages, ps, _stream()), "velox_paged_append")
+    elif q is not None:
+        out = torch.empty((N, H, d), dtype=_BF16, device=k.device)
+        po = out.data_ptr()
+    _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
+                                  spec, po, kp, vp, page, num_pages, ps, _raw_stream(index)),
+           "velox_paged_append")
     return out
 
 
@@ -617,32 +659,42 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     """One new token per request, q [R,H,d] bf16, against its first lens [R] tokens
     in k_pages / v_pages [num_pages,Hkv,page,d] bf16 by table [R,max_pages] int32
     -> (O [R,H,d] bf16, lse [R,H] f32 or None). H is a multiple of Hkv."""
-    R, H, d = q.shape
-    dev = q.device
-    pq = _arg(q, "q", torch.bfloat16, None, dev)
-    kp, vp = _pool(k_pages, v_pages, dev)
-    num_pages, Hkv, page, dp = k_pages.shape
+    R, H, d = shape = q.shape
+    index = q.get_device()
+    pq = _arg(q, "q", _BF16, None, index)
+    num_pages, Hkv, page, dp = pages = k_pages.shape
     if dp != d:
         raise ValueError(f"q has heads of {d}, the pages of {dp}")
-    if table.dim() != 2 or table.shape[0] != R:
+    kp = _arg(k_pages, "k_pages", _BF16, None, index)
+    vp = _arg(v_pages, "v_pages", _BF16, pages, index)
+    tr, width = table.shape
+    if tr != R:
         raise ValueError(f"table must be [{R},max_pages]")
-    pt = _arg(table, "table", torch.int32, None, dev)
-    pl = _arg(lens, "lens", torch.int32, (R,), dev)
-    ps = _arg(status, "status", torch.int32, None, dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _guard(q, stream):
-        if ws is None:
-            ws = paged_attn_workspace(R, H, Hkv, d, dev)
-        if out is None:
-            out = torch.empty((R, H, d), dtype=torch.bfloat16, device=dev)
-        if not want_lse:
-            lse = None
-        elif lse is None:
-            lse = torch.empty((R, H), dtype=torch.float32, device=dev)
-        _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages,
-                                    table.shape[1], float(scale),
-                                    _arg(out, "out", torch.bfloat16, (R, H, d), dev),
-                                    _arg(lse, "lse", torch.float32, (R, H), dev),
-                                    _arg(ws, "ws", torch.uint8, None, dev), ws.numel(), ps,
-                                    _stream()), "velox_paged_attn")
+    pt = _arg(table, "table", _I32, None, index)
+    pl = _arg(lens, "lens", _I32, (R,), index)
+    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    there = _elsewhere(q, stream)
+    if there is not None:
+        with there:
+            return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status)
+    if ws is None:
+        ws = paged_attn_workspace(R, H, Hkv, d, q.device)
+        pw = ws.data_ptr()
+    else:
+        pw = _arg(ws, "ws", torch.uint8, None, index)
+    if out is None:
+        out = torch.empty_like(q)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", _BF16, shape, index)
+    if not want_lse:
+        lse = pe = None
+    elif lse is None:
+        lse = torch.empty((R, H), dtype=_F32, device=q.device)
+        pe = lse.data_ptr()
+    else:
+        pe = _arg(lse, "lse", _F32, (R, H), index)
+    _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
+                                1.0 / math.sqrt(d) if scale is None else scale, po, pe, pw,
+                                ws.numel(), ps, _raw_stream(index)), "velox_paged_attn")
     return out, lse
