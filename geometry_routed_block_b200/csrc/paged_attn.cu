@@ -45,6 +45,8 @@ constexpr int UNIT = 16;       // tokens per unit: the smallest page
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most (two per SM)
+constexpr int JT = 256;        // threads of the joining kernel
+constexpr int JW = JT / 32;
 constexpr int ROW_COST = 1;    // empty units that a row counts for
 // units per warp at least: fewer would cost more joining than they save
 constexpr int MIN_SHARE = 2;
@@ -61,8 +63,12 @@ struct Cfg {
     static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][HEADS][D]: a warp's first row
     static constexpr int OFF_M = OFF_O + NW * HEADS * D * 4;   // float [2 NW][HEADS]
     static constexpr int OFF_L = OFF_M + 2 * NW * HEADS * 4;   // float [2 NW][HEADS]
-    static constexpr int OFF_SH = OFF_L + 2 * NW * HEADS * 4;  // int64 [NW][6]
-    static constexpr int OFF_BAR = OFF_SH + NW * 6 * 8;        // uint64 [NW][ST]
+    // where the shares' rows are found, int64 [NW][6]; at the end the rows' maxima, float
+    // [2 NW][HEADS]
+    static constexpr int OFF_SH = OFF_L + 2 * NW * HEADS * 4;
+    static constexpr int OFF_TOP = OFF_SH;
+    static constexpr int OFF_BAR = OFF_SH + 2 * NW * HEADS * 4;  // uint64 [NW][ST]
+    static_assert(2 * HEADS * 4 >= 6 * 8, "room for the shares' rows");
     static constexpr int OFF_ENT = OFF_BAR + NW * ST * 8;      // int [2 NW][4]: the parts
     static constexpr int OFF_ABORT = OFF_ENT + 2 * NW * 16;
     static constexpr int SMEM = OFF_ABORT + 8;
@@ -92,12 +98,13 @@ __device__ __forceinline__ int weight(int units) { return units > 0 ? units + RO
 
 // Every thread of the CTA calls it. Counts the work, and finds the rows in which `count`
 // shares begin, from the first-th of grid * per on: sh[6 w] onwards gets share
-// w's row. sh: 6 long longs per share, NW of them at least. The caller lets the CTA
+// w's row. sh: 6 long longs per share, and one per warp at least. The caller lets the CTA
 // meet before it reads sh.
+template <int THREADS>
 __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, int count, int per,
                                        long long* sh, bool report) {
     const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
-    const int each = (a.R + NT - 1) / NT;
+    const int each = (a.R + THREADS - 1) / THREADS;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * each), r1 = min(a.R, r0 + each);
     long long mine = 0;
     bool bad = false;
@@ -118,7 +125,7 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, 
     __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += sh[w];
         all += sh[w];
     }
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
 
     const int cta = blockIdx.x;
-    const Work work = locate(a, cta * NW, NW, NW, sh, cta == 0);
+    const Work work = locate<NT>(a, cta * NW, NW, NW, sh, cta == 0);
     __syncthreads();  // rows found, barriers initialised
     if (cta >= work.grid || work.total == 0) return;
     // this warp's share: units g0 .. g1 - 1
@@ -499,121 +506,197 @@ __global__ void __launch_bounds__(NT, 2)
     // in this CTA
     __syncthreads();
     const int* ents = reinterpret_cast<const int*>(smem + C::OFF_ENT);
-    const float* sm_m = reinterpret_cast<const float*>(smem + C::OFF_M);
-    const float* sm_l = reinterpret_cast<const float*>(smem + C::OFF_L);
-    for (int e0 = 0; e0 < 2 * NW; ++e0) {
-        if (ents[4 * e0] < 0) continue;
-        int e1 = e0;  // last entry of the row
-        bool ends = (e0 & 1) == 0;
-        for (int e = e0 + 1; e < 2 * NW && !ends; ++e)
-            if (ents[4 * e] >= 0) e1 = e, ends = (e & 1) == 0;
+    float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
+    float* sm_l = reinterpret_cast<float*>(smem + C::OFF_L);
+    float* sm_top = reinterpret_cast<float*>(smem + C::OFF_TOP);
+    // thread (e, h): entry e's weight in its row, for query head h; with the row's
+    // first entry also the row's maximum and sum. Bit e of `have` is an entry, of
+    // `enders` one that ends its row
+    uint32_t have = 0;
+#pragma unroll
+    for (int e = 0; e < 2 * NW; ++e) have |= (ents[4 * e] >= 0 ? 1u : 0u) << e;
+    if (!have) return;
+    const uint32_t enders = have & 0x55555555u;
+    const auto last_of = [&](int e) {  // last entry of e's row
+        const uint32_t end = enders & (~0u << e);
+        return end ? __ffs(end) - 1 : 31 - __clz(have);
+    };
+    const int te = threadIdx.x / C::HEADS, th = threadIdx.x % C::HEADS;
+    float weight_e = 0.0f, row_sum = 0.0f, top = -INFINITY;
+    const bool mine_e = te < 2 * NW && (have >> te & 1);
+    if (mine_e) {
+        const uint32_t below = enders & ((1u << te) - 1);  // the row before e's
+        const int from = below ? 32 - __clz(below) : 0, to = last_of(te);
+        for (int e = from; e <= to; ++e)
+            if (have >> e & 1) top = fmaxf(top, sm_m[e * C::HEADS + th]);
+        const float ref = top == -INFINITY ? 0.0f : top;
+        weight_e = ex2_approx(sm_m[te * C::HEADS + th] - ref);
+        for (int e = from; e <= to; ++e)
+            if (have >> e & 1)
+                row_sum += ex2_approx(sm_m[e * C::HEADS + th] - ref) * sm_l[e * C::HEADS + th];
+    }
+    __syncthreads();
+    if (mine_e) {
+        sm_m[te * C::HEADS + th] = weight_e;
+        sm_l[te * C::HEADS + th] = row_sum;
+        sm_top[te * C::HEADS + th] = top;
+    }
+    __syncthreads();
+    for (uint32_t left = have; left;) {
+        const int e0 = __ffs(left) - 1, e1 = last_of(e0);
+        const bool begins = ents[4 * e0 + 3] != 0, ends = (e1 & 1) == 0;
         const int r = ents[4 * e0 + 1], row = ents[4 * e0 + 2];
-        const bool begins = ents[4 * e0 + 3] != 0;
         const int hk = row / a.head_tiles, ht = row - hk * a.head_tiles;
         const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
         const long long q_row =
             static_cast<long long>(r) * a.H + hk * a.group + ht * a.tile_heads;
         float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
-        for (int i = threadIdx.x; i < heads * D; i += NT) {
-            const int h = i / D, col = i % D;
-            float top = -INFINITY;
-            for (int e = e0; e <= e1; ++e)
-                if (ents[4 * e] >= 0) top = fmaxf(top, sm_m[e * C::HEADS + h]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f, acc = 0.0f;
-            for (int e = e0; e <= e1; ++e)
-                if (ents[4 * e] >= 0) {
-                    const float x = ex2_approx(sm_m[e * C::HEADS + h] - ref);
-                    sum += x * sm_l[e * C::HEADS + h];
-                    acc += x * part_o<D, MT>(smem, e)[h * D + col];
+        for (int i = threadIdx.x; i < heads * (D / 4); i += NT) {
+            const int h = i / (D / 4), col = 4 * (i % (D / 4));
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 2 * NW; ++e)
+                if (e >= e0 && e <= e1 && (have >> e & 1)) {
+                    const float x = sm_m[e * C::HEADS + h];
+                    const float4 v =
+                        *reinterpret_cast<const float4*>(part_o<D, MT>(smem, e) + h * D + col);
+                    acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
                 }
+            const float sum = sm_l[e0 * C::HEADS + h], m_row = sm_top[e0 * C::HEADS + h];
             if (begins && ends) {
-                a.o[(q_row + h) * D + col] = __float2bfloat16_rn(acc / sum);
-                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top, sum);
+                const float inv = 1.0f / sum;
+                *reinterpret_cast<uint2*>(a.o + (q_row + h) * D + col) = make_uint2(
+                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(m_row, sum);
             } else {
-                part[h * D + col] = acc;
+                *reinterpret_cast<float4*>(part + h * D + col) = acc;
                 if (col == 0) {
-                    part[C::HEADS * D + h] = top;
+                    part[C::HEADS * D + h] = m_row;
                     part[C::HEADS * D + C::HEADS + h] = sum;
                 }
             }
         }
-        e0 = e1;
+        left &= e1 == 31 ? 0u : ~0u << (e1 + 1);
     }
 }
 
-// Joins the parts of the rows that more than one CTA worked on. CTA (c - 1, head):
-// where share c begins inside a row, and is the first to do so, one query head of
-// that row. The row's parts are those of consecutive shares; the order of the
-// sums is fixed.
+// Joins the parts of the rows that more than one CTA worked on. CTA c stands for share
+// c, and the n shares of a row divide its query heads: heads i, i + n, ... fall to
+// the i-th. Where there are more heads than shares (few parts each), a warp joins a
+// head alone; where there are more shares (many parts), the CTA's warps take parts
+// of one head in turn and meet in shared memory. The order of the sums is fixed.
 template <int D, int MT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(JT)
     paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
     using C = Cfg<D, MT>;
-    __shared__ long long sh[6 * NW];
-    __shared__ float red_m[NW], red_l[NW], red_o[NW][D];
-    const int c = blockIdx.x + 1, hh = blockIdx.y;
-    const Work work = locate(a, c, 1, 1, sh, false);
+    constexpr int LANES = D / 4, SUB = 32 / LANES;  // lanes of a part, parts at a time
+    __shared__ long long sh[6 * JW];
+    __shared__ float red_m[JW], red_l[JW];
+    __shared__ float4 red_o[JW][LANES];
+    const int c = blockIdx.x;
+    const Work work = locate<JT>(a, c, 2, 1, sh, false);
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c >= work.grid || work.total == 0) return;
-    const Row p = located(sh);
-    const long long s = share(work.total, work.grid, c), end = p.base + p.units;
-    if (s <= p.base || s >= end || share(work.total, work.grid, c - 1) > p.base) return;
-    const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
-    const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
-    if (hh >= heads) return;
-    // the last share that begins before the row's end
-    const int last = static_cast<int>((end * work.grid - 1) / work.total);
-    const int first = c - 1;
+    const long long s0 = share(work.total, work.grid, c), s1 = share(work.total, work.grid, c + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int PER = D / 32;
 
-    float top = -INFINITY, sum = 0.0f, acc[PER];
+    // the row that share c goes on with, and the one it begins and leaves
+    for (int side = 0; side < 2; ++side) {
+        if (side == 1 && c + 1 >= work.grid) break;
+        const Row p = located(sh + 6 * side);
+        const long long end = p.base + p.units;
+        if (side == 0 ? (s0 <= p.base || s0 >= end) : (p.base < s0 || s1 <= p.base || s1 >= end))
+            continue;
+        const int first = static_cast<int>(((p.base + 1) * work.grid - 1) / work.total);
+        const int n = static_cast<int>((end * work.grid - 1) / work.total) - first + 1;
+        const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
+        const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
+        const long long q_row = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
+        const bool team = n >= heads;  // the whole CTA on one head
+        const int step = team ? JW : 1;
+        for (int hh = c - first + (team ? 0 : n * warp); hh < heads; hh += team ? n : n * JW) {
+            // this warp's parts: i0, i0 + step, ...; lane j looks after the j-th and the
+            // j + 32-th (a team's warp has at most MAX_GRID / JW, a lone one 15)
+            const int i0 = team ? warp : 0, mine = i0 < n ? (n - 1 - i0) / step + 1 : 0;
+            // part 1 of the share in which the row begins, part 0 of the others
+            const auto part_at = [&](int j) {
+                const int i = i0 + j * step;
+                return a.part + static_cast<long long>(2 * (first + i) + (i == 0 ? 1 : 0)) * C::PART;
+            };
+            float m[2], l[2], w[2], top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
-    for (int i = first + warp; i <= last; i += NW) {
-        // part 1 of the share in which the row begins, part 0 of the others
-        const int which = 2 * i + (share(work.total, work.grid, i) <= p.base ? 1 : 0);
-        const float* part = a.part + static_cast<long long>(which) * C::PART;
-        const float m = part[C::HEADS * D + hh], l = part[C::HEADS * D + C::HEADS + hh];
-        float v[PER];
+            for (int k = 0; k < 2; ++k) {
+                m[k] = -INFINITY, l[k] = 0.0f;
+                if (lane + 32 * k < mine) {
+                    const float* part = part_at(lane + 32 * k);
+                    m[k] = part[C::HEADS * D + hh];
+                    l[k] = part[C::HEADS * D + C::HEADS + hh];
+                }
+                top = fmaxf(top, m[k]);
+            }
 #pragma unroll
-        for (int e = 0; e < PER; ++e) v[e] = part[hh * D + lane + 32 * e];
-        const float m_new = fmaxf(top, m);
-        const float ref = m_new == -INFINITY ? 0.0f : m_new;
-        const float x = ex2_approx(top - ref), y = ex2_approx(m - ref);
-        sum = sum * x + l * y;
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = acc[e] * x + v[e] * y;
-        top = m_new;
-    }
-    if (lane == 0) red_m[warp] = top, red_l[warp] = sum;
+            for (int k = 0; k < 2; ++k) {
+                w[k] = ex2_approx(m[k] - ref);
+                sum += w[k] * l[k];
+            }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) red_o[warp][lane + 32 * e] = acc[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float m = red_m[0];
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int sub = lane / LANES, col = 4 * (lane % LANES);
+#pragma unroll 8
+            for (int j = 0; j < mine; j += SUB) {
+                const int at = j + sub;
+                const float x = __shfl_sync(~0u, at < 32 ? w[0] : w[1], at & 31);
+                if (at < mine) {
+                    const float4 v =
+                        *reinterpret_cast<const float4*>(part_at(at) + hh * D + col);
+                    acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+                }
+            }
+            if (SUB == 2) {
+                acc.x += __shfl_xor_sync(~0u, acc.x, 16), acc.y += __shfl_xor_sync(~0u, acc.y, 16);
+                acc.z += __shfl_xor_sync(~0u, acc.z, 16), acc.w += __shfl_xor_sync(~0u, acc.w, 16);
+            }
+            if (team) {
+                if (lane == 0) red_m[warp] = top, red_l[warp] = sum;
+                if (sub == 0) red_o[warp][lane] = acc;
+                __syncthreads();
+                if (warp == 0) {
+                    top = red_m[0];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) m = fmaxf(m, red_m[w]);
-        const float ref = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, o = 0.0f;
+                    for (int k = 1; k < JW; ++k) top = fmaxf(top, red_m[k]);
+                    const float all = top == -INFINITY ? 0.0f : top;
+                    sum = 0.0f;
+                    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float x = ex2_approx(red_m[w] - ref);
-            l += x * red_l[w];
-            o += x * red_o[w][threadIdx.x];
+                    for (int k = 0; k < JW; ++k) {
+                        const float x = ex2_approx(red_m[k] - all);
+                        const float4 v = red_o[k][lane % LANES];
+                        sum += x * red_l[k];
+                        acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+                    }
+                }
+                __syncthreads();
+            }
+            if ((!team || warp == 0) && sub == 0) {
+                const float inv = 1.0f / sum;
+                *reinterpret_cast<uint2*>(a.o + (q_row + hh) * D + col) = make_uint2(
+                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                if (a.lse && lane == 0) a.lse[q_row + hh] = log_sum(top, sum);
+            }
         }
-        const long long row =
-            static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads + hh;
-        a.o[row * D + threadIdx.x] = __float2bfloat16_rn(o / l);
-        if (a.lse && threadIdx.x == 0) a.lse[row] = log_sum(m, l);
     }
 }
 
 template <int D, int MT>
 int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream_t st) {
     using C = Cfg<D, MT>;
+    static_assert((MAX_GRID + JW - 1) / JW <= 64, "parts of a joining warp");
     static_assert(C::SMEM + 1024 <= 233472 / 2, "shared memory of two CTAs");
     static_assert(C::HALF % 1024 == 0, "swizzle atoms");
     CUtensorMap tk, tv;
@@ -624,16 +707,21 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return VELOX_ECUDA;
-    a.grid = std::min(2 * sms, MAX_GRID);
+    // two CTAs per SM, but no more than the longest histories could keep busy
+    const long long most = static_cast<long long>(a.R) * a.Hkv * a.head_tiles *
+                           (static_cast<long long>(a.max_pages) * a.page / UNIT + ROW_COST);
+    a.grid = static_cast<int>(std::min<long long>(std::min(2 * sms, MAX_GRID),
+                                                  (most + NW * MIN_SHARE - 1) / (NW * MIN_SHARE)));
     auto kern = paged_attn_kernel<D, MT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
         return VELOX_ECUDA;
     kern<<<a.grid, NT, C::SMEM, st>>>(tk, tv, a);
     if (cudaGetLastError() != cudaSuccess) return VELOX_ECUDA;
+    if (a.grid == 1) return VELOX_OK;  // no row is shared
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(a.grid - 1, a.tile_heads);
-    cfg.blockDim = dim3(NT);
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(JT);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
