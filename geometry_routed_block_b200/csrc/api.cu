@@ -526,7 +526,7 @@ int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, co
                      const int32_t* lens, int R, int H, int Hkv, int d, int page, int num_pages,
                      int max_pages, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
                      int32_t* status, void* stream) {
-    if (!q || !k_pages || !v_pages || !table || !lens || !o || !ws) return VELOX_EINVAL;
+    if (!q || !k_pages || !v_pages || !table || !lens || !o) return VELOX_EINVAL;
     if (R < 1 || R > 65535 || Hkv < 1 || H < Hkv || H % Hkv || d < 1 || page < 1 ||
         num_pages < 1 || max_pages < 1)
         return VELOX_EINVAL;
@@ -541,7 +541,9 @@ int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, co
         static_cast<long long>(num_pages) * page * Hkv >= INT_LIMIT ||
         static_cast<long long>(R) * H >= INT_LIMIT)
         return VELOX_EINVAL;
-    if (ws_bytes < velox_paged_attn_workspace_size(R, H, Hkv, d)) return VELOX_EINVAL;
+    if (!velox::paged_attn_whole(R, H, Hkv, page, max_pages) &&
+        (!ws || ws_bytes < velox_paged_attn_workspace_size(R, H, Hkv, d)))
+        return VELOX_EINVAL;
 
     velox::PagedAttnArgs a{};
     a.q = static_cast<const __nv_bfloat16*>(q);

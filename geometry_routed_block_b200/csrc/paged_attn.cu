@@ -51,6 +51,12 @@ constexpr int ROW_COST = 1;    // empty units that a row counts for
 // units per warp at least: fewer would cost more joining than they save
 constexpr int MIN_SHARE = 2;
 
+// Where no row can be longer than this (by the width of the table) and there are no
+// more rows than CTAs fit on the GPU at once, a CTA takes a row, and nothing is joined.
+// Measured at 512 tokens: 8.7 to 10.2 us, split 8.4 to 9.3 us; at 64 tokens 4.1 and 8.3 us;
+// at 1024 tokens 13.3 and 8.5 us (one launch less on the host besides).
+constexpr int WHOLE_UNITS = 32, WHOLE_ROWS = 256;
+
 template <int D, int MT>
 struct Cfg {
     static constexpr int HEADS = 8 * MT;           // query heads per tile
@@ -63,12 +69,8 @@ struct Cfg {
     static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][HEADS][D]: a warp's first row
     static constexpr int OFF_M = OFF_O + NW * HEADS * D * 4;   // float [2 NW][HEADS]
     static constexpr int OFF_L = OFF_M + 2 * NW * HEADS * 4;   // float [2 NW][HEADS]
-    // where the shares' rows are found, int64 [NW][6]; at the end the rows' maxima, float
-    // [2 NW][HEADS]
-    static constexpr int OFF_SH = OFF_L + 2 * NW * HEADS * 4;
-    static constexpr int OFF_TOP = OFF_SH;
-    static constexpr int OFF_BAR = OFF_SH + 2 * NW * HEADS * 4;  // uint64 [NW][ST]
-    static_assert(2 * HEADS * 4 >= 6 * 8, "room for the shares' rows");
+    static constexpr int OFF_SH = OFF_L + 2 * NW * HEADS * 4;  // int64 [NW][6]: shares' rows
+    static constexpr int OFF_BAR = OFF_SH + NW * 6 * 8;        // uint64 [NW][ST]
     static constexpr int OFF_ENT = OFF_BAR + NW * ST * 8;      // int [2 NW][4]: the parts
     static constexpr int OFF_ABORT = OFF_ENT + 2 * NW * 16;
     static constexpr int SMEM = OFF_ABORT + 8;
@@ -86,22 +88,40 @@ struct Row {
     int r, row;     // request, row in it
     int n, units;   // tokens and units of the request
 };
+// The total (the empty units included) in equal shares, NW to a CTA: `more` of each
+// + 1 units, then of `each`.
 struct Work {
-    long long total;  // units, the empty ones included
-    int grid;         // CTAs that take a share
+    long long total, each;
+    int grid;  // CTAs that take a share
+    int more;
+    // where warp share w begins
+    __device__ __forceinline__ long long start(int w) const { return w * each + min(w, more); }
+    // the CTA in whose share unit u lies
+    __device__ __forceinline__ int cta_of(long long u) const;
 };
 
-// where share c of n begins
-__device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
+// 64-bit division, 32-bit wherever the numbers are: several of the former are what
+// a short call would spend most of its time on
+__device__ __forceinline__ long long quotient(long long x, long long d) {
+    if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+    return x / d;
+}
+
+__device__ __forceinline__ int Work::cta_of(long long u) const {
+    const long long first = more * (each + 1);
+    const long long w = u < first ? quotient(u, each + 1) : more + quotient(u - first, each);
+    return static_cast<int>(w) / NW;
+}
 
 __device__ __forceinline__ int weight(int units) { return units > 0 ? units + ROW_COST : 0; }
 
-// Every thread of the CTA calls it. Counts the work, and finds the rows in which `count`
-// shares begin, from the first-th of grid * per on: sh[6 w] onwards gets share
-// w's row. sh: 6 long longs per share, and one per warp at least. The caller lets the CTA
-// meet before it reads sh.
+// Every thread of the CTA calls it. Counts the work, and finds the rows in which
+// `count` warp shares begin, those numbered first, first + step, ...: sh[6 i] onwards
+// gets the i-th's row (nothing where there is no such share, or an empty one at the
+// end). sh: 6 long longs per share, and one per warp at least. The caller lets the
+// CTA meet before it reads sh.
 template <int THREADS>
-__device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, int count, int per,
+__device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int count, int step,
                                        long long* sh, bool report) {
     const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
     const int each = (a.R + THREADS - 1) / THREADS;
@@ -134,10 +154,12 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, 
     k.total = all * rows;
     const long long most = (k.total + NW * MIN_SHARE - 1) / (NW * MIN_SHARE);
     k.grid = static_cast<int>(min(static_cast<long long>(a.grid), max(most, 1ll)));
+    k.each = quotient(k.total, k.grid * NW);
+    k.more = static_cast<int>(k.total - k.each * (k.grid * NW));
     const long long from = (before + x - mine) * rows, to = from + mine * rows;
     for (int w = 0; w < count; ++w) {
-        if (first_share + w >= k.grid * per) break;
-        const long long s = share(k.total, k.grid * per, first_share + w);
+        if (first + w * step >= k.grid * NW) break;
+        const long long s = k.start(first + w * step);
         if (s < from || s >= to) continue;
         long long at = from;
         int r = r0, un = 0, n = 0;
@@ -148,7 +170,7 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first_share, 
             if (s < next) break;
             at = next;
         }
-        const int row = static_cast<int>((s - at) / weight(un));
+        const int row = static_cast<int>(quotient(s - at, weight(un)));
         sh[6 * w] = at + static_cast<long long>(row) * weight(un);
         sh[6 * w + 1] = r;
         sh[6 * w + 2] = row;
@@ -225,6 +247,21 @@ __device__ __forceinline__ float log_sum(float m, float l) {
     return ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
 }
 
+// zeros for the requests r, r + step, ... that have no tokens
+template <int D>
+__device__ __forceinline__ void empty_rows(const PagedAttnArgs& a, int r, int step, int cap) {
+    const int elems = a.H * D;
+    for (; r < a.R; r += step) {
+        if (clamp_len(a.lens[r], cap) > 0) continue;
+        for (int i = threadIdx.x; i < elems / 8; i += NT)
+            reinterpret_cast<uint4*>(a.o + static_cast<long long>(r) * elems)[i] =
+                make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int h = threadIdx.x; h < a.H; h += NT)
+                a.lse[static_cast<long long>(r) * a.H + h] = -INFINITY;
+    }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(NT, 2)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -253,26 +290,33 @@ __global__ void __launch_bounds__(NT, 2)
         for (int s = 0; s < C::ST; ++s) mbar_init(bars + 8 * s, 1);
     fence_mbar_init();
 
-    // requests without tokens get zeros
-    const int row_elems = a.H * D;
-    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
-        if (clamp_len(a.lens[r], cap) > 0) continue;
-        for (int i = threadIdx.x; i < row_elems / 8; i += NT)
-            reinterpret_cast<uint4*>(a.o + static_cast<long long>(r) * row_elems)[i] =
-                make_uint4(0, 0, 0, 0);
-        if (a.lse)
-            for (int h = threadIdx.x; h < a.H; h += NT)
-                a.lse[static_cast<long long>(r) * a.H + h] = -INFINITY;
+    const int cta = blockIdx.x, rows = a.Hkv * a.head_tiles;
+    long long g0, g1;  // this warp's share: units g0 .. g1 - 1
+    Row p;
+    if (a.whole_rows) {
+        // one row per CTA, a quarter of it per warp
+        p.base = 0;
+        p.r = cta / rows;
+        p.row = cta - p.r * rows;
+        const int n = a.lens[p.r];
+        p.n = clamp_len(n, cap);
+        p.units = units_of(p.n);
+        if (p.row == 0 && threadIdx.x == 0 && n != p.n && a.status)
+            atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
+        g0 = p.units * warp / NW, g1 = p.units * (warp + 1) / NW;
+        __syncthreads();  // barriers initialised
+        if (p.n == 0 && p.row == 0) empty_rows<D>(a, p.r, a.R, cap);
+        if (p.n == 0) return;
+    } else {
+        const Work work = locate<NT>(a, cta * NW, NW, 1, sh, cta == 0);
+        __syncthreads();  // rows found, barriers initialised
+        if (cta >= work.grid || work.total == 0) {
+            empty_rows<D>(a, cta, gridDim.x, cap);
+            return;
+        }
+        g0 = work.start(cta * NW + warp), g1 = work.start(cta * NW + warp + 1);
+        p = located(sh + 6 * warp);
     }
-
-    const int cta = blockIdx.x;
-    const Work work = locate<NT>(a, cta * NW, NW, NW, sh, cta == 0);
-    __syncthreads();  // rows found, barriers initialised
-    if (cta >= work.grid || work.total == 0) return;
-    // this warp's share: units g0 .. g1 - 1
-    const long long g0 = share(work.total, work.grid * NW, cta * NW + warp);
-    const long long g1 = share(work.total, work.grid * NW, cta * NW + warp + 1);
-    Row p = located(sh + 6 * warp);
 
     // ---- loads, ahead of the products and across rows
     Row f = p;
@@ -315,13 +359,15 @@ __global__ void __launch_bounds__(NT, 2)
             ++ahead;
         }
 
+    if (!a.whole_rows) empty_rows<D>(a, cta, gridDim.x, cap);  // while the loads are on their way
+
     const int g = lane >> 2, t = lane & 3;
     int* ent = reinterpret_cast<int*>(smem + C::OFF_ENT) + 8 * warp;  // this warp's two parts
     if (lane < 2) ent[4 * lane] = -1;  // none yet
     int slot = 0;
     uint32_t parity = 0;
     bool ok = true;
-    while (true) {
+    while (g0 < g1) {
         // units of this row in the share
         const int u0 = static_cast<int>(max(g0 - p.base, 0ll));
         const int u1 = static_cast<int>(min(g1 - p.base, static_cast<long long>(p.units)));
@@ -506,45 +552,17 @@ __global__ void __launch_bounds__(NT, 2)
     // in this CTA
     __syncthreads();
     const int* ents = reinterpret_cast<const int*>(smem + C::OFF_ENT);
-    float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
-    float* sm_l = reinterpret_cast<float*>(smem + C::OFF_L);
-    float* sm_top = reinterpret_cast<float*>(smem + C::OFF_TOP);
-    // thread (e, h): entry e's weight in its row, for query head h; with the row's
-    // first entry also the row's maximum and sum. Bit e of `have` is an entry, of
-    // `enders` one that ends its row
-    uint32_t have = 0;
+    const float* sm_m = reinterpret_cast<const float*>(smem + C::OFF_M);
+    const float* sm_l = reinterpret_cast<const float*>(smem + C::OFF_L);
+    uint32_t left = 0;  // bit e: an entry
 #pragma unroll
-    for (int e = 0; e < 2 * NW; ++e) have |= (ents[4 * e] >= 0 ? 1u : 0u) << e;
-    if (!have) return;
-    const uint32_t enders = have & 0x55555555u;
-    const auto last_of = [&](int e) {  // last entry of e's row
-        const uint32_t end = enders & (~0u << e);
-        return end ? __ffs(end) - 1 : 31 - __clz(have);
-    };
-    const int te = threadIdx.x / C::HEADS, th = threadIdx.x % C::HEADS;
-    float weight_e = 0.0f, row_sum = 0.0f, top = -INFINITY;
-    const bool mine_e = te < 2 * NW && (have >> te & 1);
-    if (mine_e) {
-        const uint32_t below = enders & ((1u << te) - 1);  // the row before e's
-        const int from = below ? 32 - __clz(below) : 0, to = last_of(te);
-        for (int e = from; e <= to; ++e)
-            if (have >> e & 1) top = fmaxf(top, sm_m[e * C::HEADS + th]);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        weight_e = ex2_approx(sm_m[te * C::HEADS + th] - ref);
-        for (int e = from; e <= to; ++e)
-            if (have >> e & 1)
-                row_sum += ex2_approx(sm_m[e * C::HEADS + th] - ref) * sm_l[e * C::HEADS + th];
-    }
-    __syncthreads();
-    if (mine_e) {
-        sm_m[te * C::HEADS + th] = weight_e;
-        sm_l[te * C::HEADS + th] = row_sum;
-        sm_top[te * C::HEADS + th] = top;
-    }
-    __syncthreads();
-    for (uint32_t left = have; left;) {
-        const int e0 = __ffs(left) - 1, e1 = last_of(e0);
-        const bool begins = ents[4 * e0 + 3] != 0, ends = (e1 & 1) == 0;
+    for (int e = 0; e < 2 * NW; ++e) left |= (ents[4 * e] >= 0 ? 1u : 0u) << e;
+    while (left) {
+        const int e0 = __ffs(left) - 1;
+        const uint32_t enders = left & 0x55555555u;
+        const bool begins = ents[4 * e0 + 3] != 0, ends = enders != 0;
+        const uint32_t these = ends ? left & ((2u << (__ffs(enders) - 1)) - 1) : left;
+        left &= ~these;
         const int r = ents[4 * e0 + 1], row = ents[4 * e0 + 2];
         const int hk = row / a.head_tiles, ht = row - hk * a.head_tiles;
         const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
@@ -553,30 +571,33 @@ __global__ void __launch_bounds__(NT, 2)
         float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
         for (int i = threadIdx.x; i < heads * (D / 4); i += NT) {
             const int h = i / (D / 4), col = 4 * (i % (D / 4));
+            float top = -INFINITY;
+            for (uint32_t es = these; es; es &= es - 1)
+                top = fmaxf(top, sm_m[(__ffs(es) - 1) * C::HEADS + h]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int e = 0; e < 2 * NW; ++e)
-                if (e >= e0 && e <= e1 && (have >> e & 1)) {
-                    const float x = sm_m[e * C::HEADS + h];
-                    const float4 v =
-                        *reinterpret_cast<const float4*>(part_o<D, MT>(smem, e) + h * D + col);
-                    acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
-                }
-            const float sum = sm_l[e0 * C::HEADS + h], m_row = sm_top[e0 * C::HEADS + h];
+            for (uint32_t es = these; es; es &= es - 1) {
+                const int e = __ffs(es) - 1;
+                const float x = ex2_approx(sm_m[e * C::HEADS + h] - ref);
+                const float4 v =
+                    *reinterpret_cast<const float4*>(part_o<D, MT>(smem, e) + h * D + col);
+                sum += x * sm_l[e * C::HEADS + h];
+                acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+            }
             if (begins && ends) {
                 const float inv = 1.0f / sum;
                 *reinterpret_cast<uint2*>(a.o + (q_row + h) * D + col) = make_uint2(
                     pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(m_row, sum);
+                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top, sum);
             } else {
                 *reinterpret_cast<float4*>(part + h * D + col) = acc;
                 if (col == 0) {
-                    part[C::HEADS * D + h] = m_row;
+                    part[C::HEADS * D + h] = top;
                     part[C::HEADS * D + C::HEADS + h] = sum;
                 }
             }
         }
-        left &= e1 == 31 ? 0u : ~0u << (e1 + 1);
     }
 }
 
@@ -590,40 +611,58 @@ __global__ void __launch_bounds__(JT)
     paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
     using C = Cfg<D, MT>;
     constexpr int LANES = D / 4, SUB = 32 / LANES;  // lanes of a part, parts at a time
+    constexpr int AT_ONCE = 4;                      // parts of a lane loaded before their weights
     __shared__ long long sh[6 * JW];
     __shared__ float red_m[JW], red_l[JW];
     __shared__ float4 red_o[JW][LANES];
     const int c = blockIdx.x;
-    const Work work = locate<JT>(a, c, 2, 1, sh, false);
+    const Work work = locate<JT>(a, c * NW, 2, NW, sh, false);
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c >= work.grid || work.total == 0) return;
-    const long long s0 = share(work.total, work.grid, c), s1 = share(work.total, work.grid, c + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the row that share c goes on with, and the one it begins and leaves. All of this
+    // comes from the lengths, before the parts are there
+    int first[2] = {}, n[2] = {}, heads[2] = {};
+    long long q_row[2] = {};
+    if (c < work.grid && work.total > 0) {
+        const long long s0 = work.start(c * NW), s1 = work.start((c + 1) * NW);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            if (side == 1 && c + 1 >= work.grid) break;
+            const Row p = located(sh + 6 * side);
+            const long long end = p.base + p.units;
+            if (side == 0 ? (s0 <= p.base || s0 >= end)
+                          : (p.base < s0 || s1 <= p.base || s1 >= end))
+                continue;
+            first[side] = work.cta_of(p.base);
+            n[side] = work.cta_of(end - 1) - first[side] + 1;
+            const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
+            heads[side] = min(a.tile_heads, a.group - ht * a.tile_heads);
+            q_row[side] = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // the row that share c goes on with, and the one it begins and leaves
     for (int side = 0; side < 2; ++side) {
-        if (side == 1 && c + 1 >= work.grid) break;
-        const Row p = located(sh + 6 * side);
-        const long long end = p.base + p.units;
-        if (side == 0 ? (s0 <= p.base || s0 >= end) : (p.base < s0 || s1 <= p.base || s1 >= end))
-            continue;
-        const int first = static_cast<int>(((p.base + 1) * work.grid - 1) / work.total);
-        const int n = static_cast<int>((end * work.grid - 1) / work.total) - first + 1;
-        const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
-        const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
-        const long long q_row = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
-        const bool team = n >= heads;  // the whole CTA on one head
+        const int n_parts = n[side], begin = first[side], n_heads = heads[side];
+        const bool team = n_parts >= n_heads;  // the whole CTA on one head
         const int step = team ? JW : 1;
-        for (int hh = c - first + (team ? 0 : n * warp); hh < heads; hh += team ? n : n * JW) {
+        for (int hh = c - begin + (team ? 0 : n_parts * warp); hh < n_heads;
+             hh += team ? n_parts : n_parts * JW) {
             // this warp's parts: i0, i0 + step, ...; lane j looks after the j-th and the
             // j + 32-th (a team's warp has at most MAX_GRID / JW, a lone one 15)
-            const int i0 = team ? warp : 0, mine = i0 < n ? (n - 1 - i0) / step + 1 : 0;
+            const int i0 = team ? warp : 0;
+            const int mine = i0 < n_parts ? (n_parts - 1 - i0) / step + 1 : 0;
             // part 1 of the share in which the row begins, part 0 of the others
             const auto part_at = [&](int j) {
                 const int i = i0 + j * step;
-                return a.part + static_cast<long long>(2 * (first + i) + (i == 0 ? 1 : 0)) * C::PART;
+                return a.part + static_cast<long long>(2 * (begin + i) + (i == 0 ? 1 : 0)) * C::PART;
             };
+            const int sub = lane / LANES, col = 4 * (lane % LANES);
+            float4 v[AT_ONCE];
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k)
+                if (k * SUB + sub < mine)
+                    v[k] = *reinterpret_cast<const float4*>(part_at(k * SUB + sub) + hh * D + col);
             float m[2], l[2], w[2], top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -647,15 +686,20 @@ __global__ void __launch_bounds__(JT)
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int sub = lane / LANES, col = 4 * (lane % LANES);
-#pragma unroll 8
-            for (int j = 0; j < mine; j += SUB) {
-                const int at = j + sub;
-                const float x = __shfl_sync(~0u, at < 32 ? w[0] : w[1], at & 31);
-                if (at < mine) {
-                    const float4 v =
-                        *reinterpret_cast<const float4*>(part_at(at) + hh * D + col);
-                    acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+            for (int j = 0; j < mine; j += AT_ONCE * SUB) {
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const int at = j + k * SUB + sub;
+                    const float x = __shfl_sync(~0u, at < 32 ? w[0] : w[1], at & 31);
+                    if (at < mine)
+                        acc.x += x * v[k].x, acc.y += x * v[k].y, acc.z += x * v[k].z,
+                            acc.w += x * v[k].w;
+                }
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const int at = j + (AT_ONCE + k) * SUB + sub;
+                    if (at < mine)
+                        v[k] = *reinterpret_cast<const float4*>(part_at(at) + hh * D + col);
                 }
             }
             if (SUB == 2) {
@@ -685,9 +729,9 @@ __global__ void __launch_bounds__(JT)
             }
             if ((!team || warp == 0) && sub == 0) {
                 const float inv = 1.0f / sum;
-                *reinterpret_cast<uint2*>(a.o + (q_row + hh) * D + col) = make_uint2(
+                *reinterpret_cast<uint2*>(a.o + (q_row[side] + hh) * D + col) = make_uint2(
                     pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (a.lse && lane == 0) a.lse[q_row + hh] = log_sum(top, sum);
+                if (a.lse && lane == 0) a.lse[q_row[side] + hh] = log_sum(top, sum);
             }
         }
     }
@@ -707,18 +751,21 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return VELOX_ECUDA;
-    // two CTAs per SM, but no more than the longest histories could keep busy
-    const long long most = static_cast<long long>(a.R) * a.Hkv * a.head_tiles *
-                           (static_cast<long long>(a.max_pages) * a.page / UNIT + ROW_COST);
-    a.grid = static_cast<int>(std::min<long long>(std::min(2 * sms, MAX_GRID),
-                                                  (most + NW * MIN_SHARE - 1) / (NW * MIN_SHARE)));
+    const int resident = std::min(2 * sms, MAX_GRID);
+    const long long rows = static_cast<long long>(a.R) * a.Hkv * a.head_tiles;
+    const long long units = static_cast<long long>(a.max_pages) * a.page / UNIT;
+    // no more CTAs than the longest histories could keep busy
+    a.grid = static_cast<int>(
+        a.whole_rows ? rows
+                     : std::min<long long>(resident, (rows * (units + ROW_COST) + NW * MIN_SHARE - 1) /
+                                                         (NW * MIN_SHARE)));
     auto kern = paged_attn_kernel<D, MT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
         return VELOX_ECUDA;
     kern<<<a.grid, NT, C::SMEM, st>>>(tk, tv, a);
     if (cudaGetLastError() != cudaSuccess) return VELOX_ECUDA;
-    if (a.grid == 1) return VELOX_OK;  // no row is shared
+    if (a.whole_rows || a.grid == 1) return VELOX_OK;  // no row is shared
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.grid);
     cfg.blockDim = dim3(JT);
@@ -734,6 +781,11 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
 
 }  // namespace
 
+bool paged_attn_whole(int R, int H, int Hkv, int page, int max_pages) {
+    const long long rows = static_cast<long long>(R) * Hkv * ((H / Hkv + 15) / 16);
+    return rows <= WHOLE_ROWS && static_cast<long long>(max_pages) * page / UNIT <= WHOLE_UNITS;
+}
+
 size_t paged_attn_ws_bytes(int R, int H, int Hkv, int d) {
     const int mt = H / Hkv > 8 ? 2 : 1;
     return static_cast<size_t>(2 * MAX_GRID) * 8 * mt * (d + 2) * sizeof(float);
@@ -744,6 +796,7 @@ int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnA
     PagedAttnArgs a = args;
     a.group = a.H / a.Hkv;
     a.head_tiles = (a.group + 15) / 16;
+    a.whole_rows = paged_attn_whole(a.R, a.H, a.Hkv, a.page, a.max_pages);
     a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
     for (a.page_shift = 4; (1 << a.page_shift) < a.page; ++a.page_shift) {}
     const bool wide = a.group > 8;

@@ -125,6 +125,7 @@ struct PagedAttnArgs {
     int tile_heads;  // query heads per tile
     int grid;        // CTAs that share the work
     int page_shift;  // log2(page)
+    int whole_rows;  // a CTA per row
     float scale_log2;
     __nv_bfloat16* o;
     float* lse;
@@ -132,6 +133,8 @@ struct PagedAttnArgs {
     int32_t* status;
     unsigned long long wait_ns;
 };
+// whether a call is never split, and needs no workspace
+bool paged_attn_whole(int R, int H, int Hkv, int page, int max_pages);
 size_t paged_attn_ws_bytes(int R, int H, int Hkv, int d);
 int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnArgs& a, int d,
                       cudaStream_t st);

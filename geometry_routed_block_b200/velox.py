@@ -677,11 +677,13 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     if there is not None:
         with there:
             return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status)
-    if ws is None:
-        ws = paged_attn_workspace(R, H, Hkv, d, q.device)
-        pw = ws.data_ptr()
+    if ws is not None:
+        pw, nw = _arg(ws, "ws", torch.uint8, None, index), ws.numel()
+    elif width * page <= 512 and R * Hkv * ((H // max(Hkv, 1) + 15) // 16) <= 256:
+        pw, nw = None, 0  # not split: the call needs none
     else:
-        pw = _arg(ws, "ws", torch.uint8, None, index)
+        ws = paged_attn_workspace(R, H, Hkv, d, q.device)
+        pw, nw = ws.data_ptr(), ws.numel()
     if out is None:
         out = torch.empty_like(q)
         po = out.data_ptr()
@@ -696,5 +698,5 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         pe = _arg(lse, "lse", _F32, (R, H), index)
     _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
                                 1.0 / math.sqrt(d) if scale is None else scale, po, pe, pw,
-                                ws.numel(), ps, _raw_stream(index)), "velox_paged_attn")
+                                nw, ps, _raw_stream(index)), "velox_paged_attn")
     return out, lse
