@@ -274,14 +274,12 @@ int launch(const RopeArgs& a, bool vec, cudaStream_t st) {
     const long long per_cta = RT >> lanes_log2;
     const long long gx = (a.tokens + per_cta - 1) / per_cta;
     if (gx >= (1ll << 31)) return VELOX_EINVAL;
-    // The heads are split until there are two CTAs per SM, four in the half layout, whose
-    // threads form twice the angles and hold twice the rows. Queries of a chunk (24 heads
-    // of 4608 tokens, bf16): 9.3 us at 296 CTAs, 10.9 at 592, 10.9 at 888; half layout
-    // 13.7, 12.1, 14.3
-    const long long want = a.half_style ? 592 : 296;
-    const int parts = static_cast<int>(
-        std::min<long long>(std::min<long long>(std::max<long long>(1, (want + gx - 1) / gx), a.rows),
-                            65535));
+    // The heads are split until there are two CTAs per SM, and no further than four heads
+    // a thread, since each part forms its angles again. Queries of a chunk (24 heads of
+    // 4608 tokens, bf16): 9.3 us so, 10.9 us with four CTAs per SM; 48 heads of
+    // 1000 tokens in the half layout 6.3 and 8.6 us; 200 tokens 3.9 us, 4.4 us down to one head
+    const long long want = std::max<long long>(1, (296 + gx - 1) / gx);
+    const int parts = static_cast<int>(std::min<long long>({want, (a.rows + 3) / 4, 65535}));
     const int rows_per_y = (a.rows + parts - 1) / parts;
     const dim3 grid(static_cast<unsigned>(gx), (a.rows + rows_per_y - 1) / rows_per_y);
     // rows loaded at once: 128 bytes of a thread (in the half layout and float32 the
