@@ -275,6 +275,8 @@ constexpr long long INT_LIMIT = 1ll << 31;
 
 inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
+inline int log2_page(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
 // Fills the rotation of a launch; `rope` may be NULL (nothing is rotated).
 int set_rope(velox::RopeArgs& r, const velox_rope_t* rope, int d, const int32_t* pos) {
     if (!rope) {
@@ -439,7 +441,7 @@ int velox_paged_append(const void* q, const void* k, const void* v, int dtype, i
     r.pos_axis = pos_axis_stride;
     r.slots = slots;
     r.page = page;
-    for (r.page_shift = 4; (1 << r.page_shift) < page; ++r.page_shift) {}
+    r.page_shift = log2_page(page);
     r.n_slots = n_slots;
     r.status = status;
     bool vec = vec_rope(r);
@@ -481,7 +483,7 @@ int velox_paged_plan(const int32_t* add, const int32_t* lens, int32_t* table,
     a.free_count = free_count;
     a.R = R;
     a.max_pages = max_pages;
-    a.page = page;
+    a.page_shift = log2_page(page);
     a.num_pages = num_pages;
     a.n_cap = n_cap;
     a.lens_out = lens_out;
@@ -509,7 +511,7 @@ int velox_paged_release(const int32_t* done, const int32_t* lens, const int32_t*
     a.free_count = free_count;
     a.R = R;
     a.max_pages = max_pages;
-    a.page = page;
+    a.page_shift = log2_page(page);
     a.num_pages = num_pages;
     a.lens_out = lens_out;
     a.free_count_out = free_count_out;
@@ -553,6 +555,7 @@ int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, co
     a.H = H;
     a.Hkv = Hkv;
     a.page = page;
+    a.page_shift = log2_page(page);
     a.num_pages = num_pages;
     a.max_pages = max_pages;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);

@@ -798,7 +798,6 @@ int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnA
     a.head_tiles = (a.group + 15) / 16;
     a.whole_rows = paged_attn_whole(a.R, a.H, a.Hkv, a.page, a.max_pages);
     a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
-    for (a.page_shift = 4; (1 << a.page_shift) < a.page; ++a.page_shift) {}
     const bool wide = a.group > 8;
     if (d == 128)
         return wide ? launch<128, 2>(k_pages, v_pages, a, st) : launch<128, 1>(k_pages, v_pages, a, st);

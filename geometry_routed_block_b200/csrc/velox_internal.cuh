@@ -103,7 +103,8 @@ struct PlanArgs {
     int32_t* table;
     int32_t* free_list;
     const int32_t* free_count;
-    int R, max_pages, page, num_pages, n_cap;
+    int R, max_pages, page_shift, num_pages, n_cap;
+    int later;  // lengths and count are written by a kernel of their own
     int32_t* lens_out;
     int32_t* free_count_out;
     int32_t* cu;

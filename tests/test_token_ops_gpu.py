@@ -237,6 +237,50 @@ def test_plan_in_place_equals_out_of_place_and_allows_no_tokens(vx):
     assert np.array_equal(tab_n.cpu().numpy(), table)
 
 
+@pytest.mark.parametrize("R,most,pad", [(3, 40, 0), (60, 100, 40), (300, 300, 3), (2000, 90, 77)])
+@pytest.mark.parametrize("fits", [True, False])
+def test_plan_and_release_in_place_at_every_size(vx, R, most, pad, fits):
+    """One CTA, a cluster, and a grid with a second kernel: lengths and count in place, a
+    plan that fits and one that does not, then all pages back."""
+    page = 16
+    rng = np.random.default_rng(R)
+    lens, add = rng.integers(0, 200, R), rng.integers(0, most, R)
+    need = sum(-(-(a + b) // page) - -(-a // page) for a, b in zip(lens, add))
+    width = max(-(-(a + b) // page) for a, b in zip(lens, add))
+    table, free, num = plan_state(lens.tolist(), page, width, need - (0 if fits else 1), R)
+    n_cap = int(add.sum()) + pad
+    want = to.plan(add, lens, table, free, page, n_cap)
+    assert (want is not None) == fits
+    lt, ct, tab, fl = i32(lens), i32([len(free)]), i32(table), i32(free + [0] * (num - len(free)))
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    e = lambda n: torch.empty(n, dtype=I32, device="cuda")  # noqa: E731
+    out = vx.PagedPlan(e(R + 1), e(n_cap), e(n_cap), e(n_cap), lt, ct)
+    vx.paged_plan(i32(add), lt, tab, fl, ct, page, n_cap, out=out, status=status)
+    assert flags(vx, status) == (0 if fits else vx.VELOX_STATUS_NO_SPACE)
+    if fits:
+        for got, exp in zip((*out[:5], tab), want):
+            assert np.array_equal(got.cpu().numpy(), np.asarray(exp))
+        lens, table, free = want[4], want[5], want[6]
+    else:
+        assert (out.slots == -1).all() and (out.cu == 0).all()
+        assert np.array_equal(tab.cpu().numpy(), table)
+    assert lt.tolist() == list(map(int, lens)) and ct.item() == len(free)
+    done = rng.integers(0, 2, R)
+    lens, free = to.release(done, lens, table, free, page)
+    for what, code in ((done, 0), (np.ones(R, int), 0)):
+        vx.paged_release(i32(what), lt, tab, fl, ct, page, lens_out=lt, free_count_out=ct, status=status)
+        assert flags(vx, status) == code
+        assert lt.tolist() == list(map(int, lens)) and ct.item() == len(free)
+        assert fl[:len(free)].tolist() == free
+        lens, free = to.release(np.ones(R, int), lens, table, free, page)
+    assert sorted(free) == list(range(num))     # every page is free once
+    ct.fill_(num + 1)
+    lt.fill_(page)
+    vx.paged_release(i32(done), lt, tab, fl, ct, page, lens_out=lt, free_count_out=ct, status=status)
+    assert flags(vx, status) == vx.VELOX_STATUS_BAD_INDEX
+    assert (lt == page).all() and ct.item() == num + 1
+
+
 BAD_PLANS = [
     ("no page left", dict(add=[0, 200, 0]), 4),
     ("more tokens than room", dict(n_cap=4), 4),
@@ -251,7 +295,7 @@ BAD_PLANS = [
 
 
 @pytest.mark.parametrize("what,change,code", BAD_PLANS, ids=[b[0] for b in BAD_PLANS])
-@pytest.mark.parametrize("n_cap", [8, 5000])
+@pytest.mark.parametrize("n_cap", [8, 5000, 20000])
 def test_plans_that_do_not_fit_change_nothing(vx, what, change, code, n_cap):
     page, width = 16, 8
     base = [3, 20, 0]
