@@ -412,9 +412,11 @@ def _int64s(values: tuple):
 def _rows(t: torch.Tensor, name: str) -> tuple:
     """The strides of a tensor whose innermost dimension is dense, 0 along dimensions of size 1."""
     shape, stride = t.shape, t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be dense in its last dimension")
-    return tuple([st if n > 1 else 0 for n, st in zip(shape[:-1], stride)])
+    if 1 in shape:
+        return tuple([st if n > 1 else 0 for n, st in zip(shape[:-1], stride)])
+    return stride[:-1]
 
 
 def _in_dtype(t: torch.Tensor, name: str) -> int:
@@ -486,7 +488,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
         with there:
             return rope(x, pos, freqs, style, sections, mscale, inverse, out)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
         ys = (H * N * d, N * d, d)
     else:
         _arg(out, "out", x.dtype, shape, index, dense=False)
@@ -544,7 +546,7 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
         with there:
             return paged_plan(add, lens, table, free_list, free_count, page, n_cap, out, status)
     if out is None:
-        buf = torch.empty(2 * R + 2 + 3 * n_cap, dtype=_I32, device=lens.device)
+        buf = lens.new_empty(2 * R + 2 + 3 * n_cap)
         o = buf.data_ptr()
         # slots, pos and req first: their rows then start where the buffer's alignment allows
         os_, op, oq = o, o + 4 * n_cap, o + 8 * n_cap
@@ -580,7 +582,7 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
             return paged_release(done, lens, table, free_list, free_count, page, lens_out,
                                  free_count_out, status)
     if lens_out is None or free_count_out is None:
-        a, b = torch.empty(R + 1, dtype=_I32, device=lens.device).split_with_sizes((R, 1))
+        a, b = lens.new_empty(R + 1).split_with_sizes((R, 1))
         lens_out = a if lens_out is None else lens_out
         free_count_out = b if free_count_out is None else free_count_out
     _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, page, num_pages,
@@ -637,7 +639,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
         if po == pq and (dt != VELOX_BF16 or not q.is_contiguous()):
             raise ValueError("out may be q itself only where q is contiguous bf16")
     elif q is not None:
-        out = torch.empty((N, H, d), dtype=_BF16, device=k.device)
+        out = q.new_empty((N, H, d)) if dt == VELOX_BF16 else q.new_empty((N, H, d), dtype=_BF16)
         po = out.data_ptr()
     _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
                                   spec, po, kp, vp, page, num_pages, ps, _raw_stream(index)),
@@ -692,7 +694,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     if not want_lse:
         lse = pe = None
     elif lse is None:
-        lse = torch.empty((R, H), dtype=_F32, device=q.device)
+        lse = q.new_empty((R, H), dtype=_F32)
         pe = lse.data_ptr()
     else:
         pe = _arg(lse, "lse", _F32, (R, H), index)
