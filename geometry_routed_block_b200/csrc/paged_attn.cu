@@ -47,7 +47,8 @@ constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most (two per SM)
 constexpr int JT = 256;        // threads of the joining kernel
 constexpr int JW = JT / 32;
-constexpr int ROW_COST = 1;    // empty units that a row counts for
+constexpr int PPL = (MAX_GRID + JT - 1) / JT;  // parts that a lane looks after
+constexpr int ROW_COST = 2;    // empty units that a row counts for
 // units per warp at least: fewer would cost more joining than they save
 constexpr int MIN_SHARE = 2;
 
@@ -128,7 +129,18 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * each), r1 = min(a.R, r0 + each);
     long long mine = 0;
     bool bad = false;
-    for (int r = r0; r < r1; ++r) {
+    constexpr int KEPT = 4;  // lengths held in registers: a second look costs as much as the first
+    int kept[KEPT] = {};
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i)
+        if (r0 + i < r1) kept[i] = a.lens[r0 + i];
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) {
+        bad |= kept[i] < 0 || kept[i] > cap;
+        kept[i] = clamp_len(kept[i], cap);
+        mine += weight(units_of(kept[i]));
+    }
+    for (int r = r0 + KEPT; r < r1; ++r) {
         const int n = a.lens[r];
         bad |= n < 0 || n > cap;
         mine += weight(units_of(clamp_len(n, cap)));
@@ -162,14 +174,21 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
         const long long s = k.start(first + w * step);
         if (s < from || s >= to) continue;
         long long at = from;
-        int r = r0, un = 0, n = 0;
-        for (; r < r1; ++r) {
-            n = clamp_len(a.lens[r], cap);
-            un = units_of(n);
-            const long long next = at + static_cast<long long>(weight(un)) * rows;
-            if (s < next) break;
-            at = next;
+        int r = -1, un = 0, n = 0;
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) {
+            if (r >= 0) continue;
+            const long long next = at + static_cast<long long>(weight(units_of(kept[i]))) * rows;
+            if (s < next) r = r0 + i, n = kept[i];
+            else at = next;
         }
+        for (int i = r0 + KEPT; r < 0 && i < r1; ++i) {
+            n = clamp_len(a.lens[i], cap);
+            const long long next = at + static_cast<long long>(weight(units_of(n))) * rows;
+            if (s < next) r = i;
+            else at = next;
+        }
+        un = units_of(n);
         const int row = static_cast<int>(quotient(s - at, weight(un)));
         sh[6 * w] = at + static_cast<long long>(row) * weight(un);
         sh[6 * w + 1] = r;
@@ -318,28 +337,46 @@ __global__ void __launch_bounds__(NT, 2)
         p = located(sh + 6 * warp);
     }
 
-    // ---- loads, ahead of the products and across rows
+    // ---- loads, ahead of the products and across rows. f: the row of the next unit to
+    // fetch, fu .. fend - 1 what is left of it in the share. Lane i keeps the page id of
+    // the row's unit ids_at + i
     Row f = p;
-    long long fg = g0;              // next unit to fetch
-    int page_id = 0, page_row = 0;  // its page, looked up one unit ahead
-    auto find = [&]() {
-        while (fg < g1 && fg >= f.base + f.units) {  // the row's real units are over
-            fg = f.base + weight(f.units);
-            if (fg < g1) next_row(a, f);
-        }
-        if (fg >= g1) return;
-        const int tok = static_cast<int>(fg - f.base) * UNIT;
-        page_row = tok & (a.page - 1);
-        page_id = a.table[static_cast<long long>(f.r) * a.max_pages + (tok >> a.page_shift)];
+    int fu = 0, fend = 0, ids_at = 0, ids = 0;
+    bool more = g0 < g1;  // units are left to fetch
+    const auto look_up = [&]() {
+        ids_at = fu;
+        if (fu + lane < fend)
+            ids = a.table[static_cast<long long>(f.r) * a.max_pages +
+                          (((fu + lane) * UNIT) >> a.page_shift)];
     };
-    auto fetch = [&](int slot) {
+    if (more) {
+        fu = static_cast<int>(g0 - f.base);
+        fend = static_cast<int>(min(g1 - f.base, static_cast<long long>(f.units)));
+    }
+    const auto settle = [&]() {  // fu to a unit that is there, its page id to a lane
+        while (more && fu >= fend) {
+            if (f.base + weight(f.units) >= g1) {
+                more = false;
+            } else {
+                next_row(a, f);
+                fu = 0;
+                fend = static_cast<int>(min(g1 - f.base, static_cast<long long>(f.units)));
+                ids_at = -32;
+            }
+        }
+        if (more && fu - ids_at >= 32) look_up();
+    };
+    ids_at = fu - 32;
+    settle();
+    const auto fetch = [&](int slot) {
+        const int found = __shfl_sync(~0u, ids, fu - ids_at);
         if (lane == 0) {
-            int id = page_id;
+            int id = found;
             if (id < 0 || id >= a.num_pages) {
                 if (a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
                 id = 0;
             }
-            const int y = (id * a.Hkv + f.row / a.head_tiles) * a.page + page_row;
+            const int y = (id * a.Hkv + f.row / a.head_tiles) * a.page + ((fu * UNIT) & (a.page - 1));
             const uint32_t bar = bars + 8 * slot, dst = ring + slot * C::STAGE;
             mbar_arrive_expect_tx(bar, C::STAGE);
 #pragma unroll
@@ -348,13 +385,12 @@ __global__ void __launch_bounds__(NT, 2)
             for (int h = 0; h < D / 64; ++h)
                 tma_load_2d(dst + C::TILE + h * C::HALF, &tmV, bar, 64 * h, y);
         }
-        ++fg;
-        find();
+        ++fu;
+        settle();
     };
-    find();
     int ahead = 0;  // units fetched and not yet used
     for (int s = 0; s < C::ST; ++s)
-        if (fg < g1) {
+        if (more) {
             fetch(s);
             ++ahead;
         }
@@ -478,7 +514,7 @@ __global__ void __launch_bounds__(NT, 2)
                 }
                 __syncwarp();  // every lane has read the slot
                 --ahead;
-                if (fg < g1) {
+                if (more) {
                     fetch(slot);
                     ++ahead;
                 }
@@ -569,32 +605,50 @@ __global__ void __launch_bounds__(NT, 2)
         const long long q_row =
             static_cast<long long>(r) * a.H + hk * a.group + ht * a.tile_heads;
         float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
-        for (int i = threadIdx.x; i < heads * (D / 4); i += NT) {
-            const int h = i / (D / 4), col = 4 * (i % (D / 4));
-            float top = -INFINITY;
-            for (uint32_t es = these; es; es &= es - 1)
-                top = fmaxf(top, sm_m[(__ffs(es) - 1) * C::HEADS + h]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (uint32_t es = these; es; es &= es - 1) {
-                const int e = __ffs(es) - 1;
-                const float x = ex2_approx(sm_m[e * C::HEADS + h] - ref);
-                const float4 v =
-                    *reinterpret_cast<const float4*>(part_o<D, MT>(smem, e) + h * D + col);
-                sum += x * sm_l[e * C::HEADS + h];
-                acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+        // four columns of a head are an item; a thread's items go side by side
+        constexpr int ITEMS = C::HEADS * (D / 4) / NT;
+        static_assert(C::HEADS * (D / 4) % NT == 0, "items of a thread");
+        const int col = 4 * (threadIdx.x % (D / 4)), h0 = threadIdx.x / (D / 4);
+        constexpr int HSTEP = NT / (D / 4);  // item k: head h0 + k HSTEP
+        float top[ITEMS], sum[ITEMS];
+        float4 acc[ITEMS];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            top[k] = -INFINITY, sum[k] = 0.0f;
+            acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        for (uint32_t es = these; es; es &= es - 1) {
+            const float* m = sm_m + (__ffs(es) - 1) * C::HEADS + h0;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) top[k] = fmaxf(top[k], m[k * HSTEP]);
+        }
+        for (uint32_t es = these; es; es &= es - 1) {
+            const int e = __ffs(es) - 1;
+            const float* src = part_o<D, MT>(smem, e) + h0 * D + col;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const float x = ex2_approx(sm_m[e * C::HEADS + h0 + k * HSTEP] -
+                                           (top[k] == -INFINITY ? 0.0f : top[k]));
+                const float4 v = *reinterpret_cast<const float4*>(src + k * HSTEP * D);
+                sum[k] += x * sm_l[e * C::HEADS + h0 + k * HSTEP];
+                acc[k].x += x * v.x, acc[k].y += x * v.y, acc[k].z += x * v.z, acc[k].w += x * v.w;
             }
+        }
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int h = h0 + k * HSTEP;
+            if (h >= heads) break;
             if (begins && ends) {
-                const float inv = 1.0f / sum;
-                *reinterpret_cast<uint2*>(a.o + (q_row + h) * D + col) = make_uint2(
-                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top, sum);
+                const float inv = 1.0f / sum[k];
+                *reinterpret_cast<uint2*>(a.o + (q_row + h) * D + col) =
+                    make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
+                               pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top[k], sum[k]);
             } else {
-                *reinterpret_cast<float4*>(part + h * D + col) = acc;
+                *reinterpret_cast<float4*>(part + h * D + col) = acc[k];
                 if (col == 0) {
-                    part[C::HEADS * D + h] = top;
-                    part[C::HEADS * D + C::HEADS + h] = sum;
+                    part[C::HEADS * D + h] = top[k];
+                    part[C::HEADS * D + C::HEADS + h] = sum[k];
                 }
             }
         }
@@ -648,8 +702,8 @@ __global__ void __launch_bounds__(JT)
         const int step = team ? JW : 1;
         for (int hh = c - begin + (team ? 0 : n_parts * warp); hh < n_heads;
              hh += team ? n_parts : n_parts * JW) {
-            // this warp's parts: i0, i0 + step, ...; lane j looks after the j-th and the
-            // j + 32-th (a team's warp has at most MAX_GRID / JW, a lone one 15)
+            // this warp's parts: i0, i0 + step, ...; lane j looks after the j-th, the
+            // j + 32-th, ... (a team's warp has at most MAX_GRID / JW, a lone one 15)
             const int i0 = team ? warp : 0;
             const int mine = i0 < n_parts ? (n_parts - 1 - i0) / step + 1 : 0;
             // part 1 of the share in which the row begins, part 0 of the others
@@ -663,9 +717,9 @@ __global__ void __launch_bounds__(JT)
             for (int k = 0; k < AT_ONCE; ++k)
                 if (k * SUB + sub < mine)
                     v[k] = *reinterpret_cast<const float4*>(part_at(k * SUB + sub) + hh * D + col);
-            float m[2], l[2], w[2], top = -INFINITY;
+            float m[PPL], l[PPL], w[PPL], top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < PPL; ++k) {
                 m[k] = -INFINITY, l[k] = 0.0f;
                 if (lane + 32 * k < mine) {
                     const float* part = part_at(lane + 32 * k);
@@ -679,7 +733,7 @@ __global__ void __launch_bounds__(JT)
             const float ref = top == -INFINITY ? 0.0f : top;
             float sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < PPL; ++k) {
                 w[k] = ex2_approx(m[k] - ref);
                 sum += w[k] * l[k];
             }
@@ -690,7 +744,10 @@ __global__ void __launch_bounds__(JT)
 #pragma unroll
                 for (int k = 0; k < AT_ONCE; ++k) {
                     const int at = j + k * SUB + sub;
-                    const float x = __shfl_sync(~0u, at < 32 ? w[0] : w[1], at & 31);
+                    float mine_w = w[0];  // at >> 5 is the same in all lanes
+#pragma unroll
+                    for (int i = 1; i < PPL; ++i) mine_w = (at >> 5) == i ? w[i] : mine_w;
+                    const float x = __shfl_sync(~0u, mine_w, at & 31);
                     if (at < mine)
                         acc.x += x * v[k].x, acc.y += x * v[k].y, acc.z += x * v[k].z,
                             acc.w += x * v[k].w;
@@ -740,7 +797,6 @@ __global__ void __launch_bounds__(JT)
 template <int D, int MT>
 int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream_t st) {
     using C = Cfg<D, MT>;
-    static_assert((MAX_GRID + JW - 1) / JW <= 64, "parts of a joining warp");
     static_assert(C::SMEM + 1024 <= 233472 / 2, "shared memory of two CTAs");
     static_assert(C::HALF % 1024 == 0, "swizzle atoms");
     CUtensorMap tk, tv;
