@@ -419,6 +419,33 @@ def _rows(t: torch.Tensor, name: str) -> tuple:
     return stride[:-1]
 
 
+def _extent(t: torch.Tensor) -> tuple:
+    """First byte and the byte behind the last of a tensor."""
+    size = t.element_size()
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * size
+
+
+def _apart(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two tensors of a call (an input and an output) share no element: their extents do
+    not meet, or they are differently placed views of one buffer with the same strides."""
+    (a, b), (c, d) = _extent(x), _extent(y)
+    if b <= c or d <= a:
+        return True
+    if x.dtype != y.dtype or x.shape != y.shape or x.stride() != y.stride() or (c - a) % x.element_size():
+        return False
+    # a shared element is an index difference (di, dj, ..., e) that makes up for the offset
+    reach = {(c - a) // x.element_size()}
+    for n, st in sorted(zip(x.shape, x.stride()), key=lambda p: -p[1])[:-1]:
+        left = {r - i * st for r in reach for i in range(-n + 1, n)}
+        # what the smaller dimensions can still make up for
+        rest = sum((m - 1) * s2 for m, s2 in zip(x.shape, x.stride()) if s2 < st)
+        reach = {r for r in left if abs(r) <= rest}
+        if len(reach) > 4096:
+            return False
+    return all(abs(r) >= x.shape[-1] for r in reach)
+
+
 def _in_dtype(t: torch.Tensor, name: str) -> int:
     if t.dtype is _BF16:
         return VELOX_BF16
@@ -493,8 +520,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
     else:
         _arg(out, "out", x.dtype, shape, index, dense=False)
         ys = _rows(out, "out")
-        if out.data_ptr() == x.data_ptr() and ys != xs:
-            raise ValueError("out may be x itself, not another view of it")
+        if (out.data_ptr() != x.data_ptr() or ys != xs) and not _apart(x, out):
+            raise ValueError("out may be x itself, but not share some of its elements")
     batched = pos.dim() == 3
     _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, _int64s(xs), p, B * N if batched else N,
                           N if batched else 0, ctypes.byref(spec), out.data_ptr(), _int64s(ys),
@@ -636,8 +663,9 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
                                 mscale, out, status)
     if out is not None:
         po = _arg(out, "out", _BF16, (N, H, d), index)
-        if po == pq and (dt != VELOX_BF16 or not q.is_contiguous()):
-            raise ValueError("out may be q itself only where q is contiguous bf16")
+        same = po == pq and dt == VELOX_BF16 and q.is_contiguous()
+        if not (same or _apart(q, out)) or not _apart(k, out) or not _apart(v, out):
+            raise ValueError("out may be q itself (bf16, contiguous), but not share elements of q, k or v")
     elif q is not None:
         out = q.new_empty((N, H, d)) if dt == VELOX_BF16 else q.new_empty((N, H, d), dtype=_BF16)
         po = out.data_ptr()
@@ -691,6 +719,8 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         po = out.data_ptr()
     else:
         po = _arg(out, "out", _BF16, shape, index)
+        if not _apart(q, out):
+            raise ValueError("out must not share elements of q: other parts still read them")
     if not want_lse:
         lse = pe = None
     elif lse is None:

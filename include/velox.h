@@ -382,7 +382,8 @@ VELOX_API int velox_rope_freqs(int rot, double base, int kind, double factor, in
 
 /*
  * Rotary positions of a tensor.
- *   x, y  [B][H][N][d], dtype VELOX_BF16 or VELOX_F32; y may be x (with x's strides)
+ *   x, y  [B][H][N][d], dtype VELOX_BF16 or VELOX_F32; y may be x (with x's strides),
+ *         and shares no element with it otherwise
  *   xs, ys  HOST, elements between batches, heads and tokens of x and y (the
  *         innermost dimension is dense); 0 is allowed in xs alone
  *   pos   int32; token n of batch b has position
@@ -457,7 +458,8 @@ VELOX_API int velox_paged_release(const int32_t* done, const int32_t* lens, cons
  *         and v are not written. No slot may be given twice
  *   pos   int32, axis a of token n at pos[a * pos_axis_stride + n]
  *   rope  rotation of q and k, or NULL (none: pos is not read)
- *   q_out [N][H][d] bf16 output (dense; NULL without q): every row is written
+ *   q_out [N][H][d] bf16 output (dense; NULL without q): every row is written. It may
+ *         be q itself (dense bf16), and shares no element with q, k or v otherwise
  *   k_pages, v_pages [num_pages][Hkv][page][d] bf16; other rows stay as they are
  * Everything is rounded to bf16 once, after the rotation. A slot of
  * num_pages * page or more is skipped and sets VELOX_STATUS_BAD_INDEX.
@@ -484,7 +486,7 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  *   head h reads key head h / (H / Hkv)
  *   table [R][max_pages], lens [R] int32: request r attends to its first lens[r]
  *   tokens (its new token among them, once appended)
- *   o [R][H][d] bf16 output; lse [R][H] float32 output (natural log of the
+ *   o [R][H][d] bf16 output, which shares nothing with q; lse [R][H] float32 output (natural log of the
  *   softmax denominator of the scaled scores) or NULL
  *   ws  scratch of velox_paged_attn_workspace_size bytes (256-B aligned); may be
  *       NULL (ws_bytes 0) for short histories of few rows, which are not split:

@@ -569,6 +569,32 @@ def test_attn_pool_beyond_32_bit_offsets(vx):
     check_attn(o, lse, want, [n], 1 / math.sqrt(d), d)
 
 
+def test_outputs_on_inputs_are_refused(vx):
+    """What would race on the GPU: an output that shares some elements of an input."""
+    R, H, d = 2, 4, 64
+    pages = torch.zeros(4, H, 16, d, dtype=torch.bfloat16, device="cuda")
+    table, lens = i32(np.zeros((R, 2))), i32([3, 4])
+    big = torch.zeros(R + 1, H, d, dtype=torch.bfloat16, device="cuda")
+    for out in (big[:R], big[1:]):
+        with pytest.raises(ValueError, match="share"):
+            vx.paged_attn(big[:R], pages, pages, table, lens, out=out)
+    k, v = (torch.zeros(R, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for q, out in ((big[:R], big[1:]), (big[:R], k), (big[:R], v), (big[:R].float(), big[:R])):
+        if q.dtype == torch.float32:
+            continue
+        with pytest.raises(ValueError, match="share"):
+            vx.paged_append(k, v, i32([0, 1]), pages, pages, q=q, out=out)
+    x = torch.zeros(1, 2, 8, d, device="cuda")
+    f = torch.tensor(freqs_for((32,)), device="cuda")
+    y = torch.zeros(1, 3, 8, d, device="cuda")
+    with pytest.raises(ValueError, match="share"):
+        vx.rope(y[:, :2], i32(np.arange(8)), f, out=y[:, 1:])
+    qkv = torch.randn(1, 8, 4, d, device="cuda").transpose(1, 2)   # heads side by side: allowed
+    want = vx.rope(qkv[:, :2], i32(np.arange(8)), f)
+    vx.rope(qkv[:, :2], i32(np.arange(8)), f, out=qkv[:, 2:])
+    assert torch.equal(qkv[:, 2:], want) and x.sum() == 0
+
+
 # ---------------------------------------------------------------- together
 
 def test_cache_of_requests_equals_the_block_path(vx):

@@ -274,6 +274,32 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(vx):
         vx.paged_attn(q.transpose(0, 1).contiguous().transpose(0, 1), pages, pages, i(2, 4), i(2))
 
 
+def test_shared_elements_are_found(vx):
+    """_apart against the sets of addresses."""
+    buf = torch.zeros(4000, dtype=torch.bfloat16)
+    rng = np.random.default_rng(0)
+
+    def addresses(t):
+        idx = torch.arange(4000).as_strided(t.shape, t.stride(), t.storage_offset())
+        return set(idx.flatten().tolist())
+
+    seen = set()
+    for _ in range(400):
+        shape = tuple(int(i) for i in rng.integers(1, 4, 2)) + (int(rng.integers(1, 5)), 8)
+        s = [int(i) for i in rng.permutation([8, 8 * shape[2] + 8, 8 * shape[2] * shape[1] * 2 + 64])]
+        x = buf.as_strided(shape, (*s, 1), int(rng.integers(0, 300)))
+        y = buf.as_strided(shape, (*s, 1) if rng.random() < 0.8 else (600, 100, 10, 1),
+                           int(rng.integers(0, 300)))
+        apart = vx._apart(x, y)
+        shared = bool(addresses(x) & addresses(y))
+        assert not (apart and shared), (shape, s, x.storage_offset(), y.storage_offset())
+        if x.stride() == y.stride():
+            assert apart != shared
+        seen.add((apart, shared))
+    assert (True, False) in seen and (False, True) in seen
+    assert vx._apart(buf[:100], buf[100:200]) and not vx._apart(buf[:101], buf[100:201])
+
+
 # ---------------------------------------------------------------- the oracle itself
 
 def test_oracle_rope_closed_forms():
