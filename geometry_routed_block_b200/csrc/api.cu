@@ -310,14 +310,14 @@ int set_rope(velox::RopeArgs& r, const velox_rope_t* rope, int d, const int32_t*
     return VELOX_OK;
 }
 
-// 16-byte accesses of 8 elements: every row starts on 16 bytes, and the rotated
-// part is whole chunks (chunk pairs in the half layout)
+// 16-byte accesses: every row starts on 16 bytes, and the rotated part and the rest are
+// whole items of 8 elements
 bool vec_rows(const void* p, int esize, int64_t s0, int64_t s1, int64_t s2) {
     const int64_t step = 16 / esize;
     return aligned(p, 16) && s0 % step == 0 && s1 % step == 0 && s2 % step == 0;
 }
 bool vec_rope(const velox::RopeArgs& r) {
-    return r.d % 8 == 0 && r.rot % (r.half_style ? 16 : 8) == 0;
+    return r.d % 8 == 0 && r.rot % 8 == 0;
 }
 
 int paged_plan_check(const void* a, const void* b, const void* c, const void* d, const void* e,

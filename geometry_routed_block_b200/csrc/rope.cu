@@ -51,48 +51,64 @@ struct Const {
     __device__ constexpr operator bool() const { return B; }
 };
 
-// 8 consecutive elements
-template <typename T>
-struct Chunk;
-template <>
-struct Chunk<__nv_bfloat16> {
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void unpack(const uint32_t* w, float* f) {  // 8 bf16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// The 8 elements of an item: SPLIT, 4 at e0 and 4 at e1, else 8 at e0.
+template <typename T, bool SPLIT>
+struct Item;
+template <bool SPLIT>
+struct Item<__nv_bfloat16, SPLIT> {
     uint4 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        r = *reinterpret_cast<const uint4*>(p);
+    __device__ __forceinline__ void load(const __nv_bfloat16* x, int e0, int e1) {
+        if (SPLIT) {
+            const uint2 a = *reinterpret_cast<const uint2*>(x + e0);
+            const uint2 b = *reinterpret_cast<const uint2*>(x + e1);
+            r = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            r = *reinterpret_cast<const uint4*>(x + e0);
+        }
     }
     __device__ __forceinline__ void get(float* f) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        unpack(w, f);
     }
 };
-template <>
-struct Chunk<float> {
+template <bool SPLIT>
+struct Item<float, SPLIT> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
+    __device__ __forceinline__ void load(const float* x, int e0, int e1) {
+        a = *reinterpret_cast<const float4*>(x + e0);
+        b = *reinterpret_cast<const float4*>(x + (SPLIT ? e1 : e0 + 4));
     }
     __device__ __forceinline__ void get(float* f) const {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
         f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     }
 };
-
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+template <bool SPLIT>
+__device__ __forceinline__ void put(__nv_bfloat16* y, int e0, int e1, const float* f) {
+    const uint4 r = make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]), bf2(f[6], f[7]));
+    if (SPLIT) {
+        *reinterpret_cast<uint2*>(y + e0) = make_uint2(r.x, r.y);
+        *reinterpret_cast<uint2*>(y + e1) = make_uint2(r.z, r.w);
+    } else {
+        *reinterpret_cast<uint4*>(y + e0) = r;
+    }
 }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float* f) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]), bf2(f[6], f[7]));
-}
-__device__ __forceinline__ void put(float* p, const float* f) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <bool SPLIT>
+__device__ __forceinline__ void put(float* y, int e0, int e1, const float* f) {
+    *reinterpret_cast<float4*>(y + e0) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(y + (SPLIT ? e1 : e0 + 4)) = make_float4(f[4], f[5], f[6], f[7]);
 }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -142,38 +158,32 @@ __device__ __forceinline__ long long token_slot(const RopeArgs& a, long long t, 
     return s;
 }
 
-// 16-byte accesses. A row (a head of a token) is cut in items of two chunks (half
-// layout: chunks i and i + rot/16 of the rotated part, then neighbours of the rest) or
-// one (interleaved); 1 << lanes_log2 threads share a token, an item each, and keep the
-// factors of their item through all heads. What is not rotated takes the same way
-// past the arithmetic, so that a warp does not part. U rows are loaded before the
-// first is used.
-template <typename TI, typename TO, bool HALF, int U>
+// Whole items of 8 elements, four pairs: interleaved, 8 neighbours; in the half layout
+// (SPLIT) 4 neighbours of the first half of the rotated part and the 4 that belong to
+// them in the second. 1 << lanes_log2 threads share a token, an item each, and keep its
+// factors through all heads. What is not rotated takes the same way past the
+// arithmetic, so that a warp does not part. U rows are loaded before the first is
+// used.
+template <typename TI, typename TO, bool SPLIT, int U>
 __global__ void __launch_bounds__(RT)
     rope_vec_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
     const int l = threadIdx.x & ((1 << lanes_log2) - 1);
     const long long t =
         static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
-    if (t >= a.tokens) return;
+    if (t >= a.tokens || 8 * l >= a.d) return;
     const int b = static_cast<int>(t) / a.N, n = static_cast<int>(t) - b * a.N;
     const int h0 = blockIdx.y * rows_per_y, h1 = h0 + rows_per_y;
     const long long slot = token_slot(a, t, blockIdx.y == 0 && l == 0);
 
-    constexpr int NP = HALF ? 8 : 4;  // pairs of an item
-    constexpr int NC = HALF ? 2 : 1;  // chunks
-    const int turns = HALF ? a.rot >> 4 : a.rot >> 3;  // items that are rotated
-    const bool turned = l < turns;
-    // where the chunks lie; the last one may be missing, and so may the whole item
-    const int e0 = HALF && !turned ? a.rot + 16 * (l - turns) : 8 * l;
-    const int e1 = !HALF ? 0 : turned ? e0 + a.rot / 2 : e0 + 8;
-    if (e0 >= a.d) return;
-    const bool second = HALF && e1 < a.d;
-    float c[NP], s[NP];
+    const bool turned = l < a.rot >> 3;  // the item is rotated
+    const int e0 = SPLIT && turned ? 4 * l : 8 * l;
+    const int e1 = e0 + (turned ? a.rot >> 1 : 4);
+    float c[4], s[4];
     if (turned && h0 < a.rotated_rows) {
         const int32_t* pos = a.pos + b * a.pos_batch + n;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int pair = NP * l + i;
+        for (int i = 0; i < 4; ++i) {
+            const int pair = 4 * l + i;
             turn(a.freqs[pair], axis_pos(a, pos, pair), a.mscale, a.sign, c[i], s[i]);
         }
     }
@@ -187,39 +197,113 @@ __global__ void __launch_bounds__(RT)
         // ROT: rows are rotated, ALL: every element of them is
         const auto rows = [&](auto ROT, auto ALL) {
             for (int h = lo; h < hi; h += U) {
-                Chunk<TI> v[U][NC];
+                Item<TI, SPLIT> v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u < hi) v[u].load(r.x + (h + u) * r.xh, e0, e1);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (h + u < hi) {
-                        const TI* x = r.x + (h + u) * r.xh;
-                        v[u][0].load(x + e0);
-                        if (second) v[u][NC - 1].load(x + e1);
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (h + u < hi) {
-                        TO* y = r.y + (h + u) * r.yh;
-                        float f[8], g[8];
-                        v[u][0].get(f);
-                        if (HALF) v[u][NC - 1].get(g);
+                        float f[8];
+                        v[u].get(f);
                         if (ROT && (ALL || turned)) {
 #pragma unroll
-                            for (int i = 0; i < NP; ++i) {
-                                float& p = HALF ? f[i] : f[2 * i & 7];
-                                float& q = HALF ? g[i] : f[(2 * i + 1) & 7];
+                            for (int i = 0; i < 4; ++i) {
+                                float& p = f[SPLIT ? i : 2 * i];
+                                float& q = f[SPLIT ? i + 4 : 2 * i + 1];
                                 const float x0 = p, x1 = q;
                                 p = x0 * c[i] - x1 * s[i];
                                 q = x1 * c[i] + x0 * s[i];
                             }
                         }
-                        put(y + e0, f);
-                        if (second) put(y + e1, g);
+                        put<SPLIT>(r.y + (h + u) * r.yh, e0, e1, f);
                     }
             }
         };
         if (!a.g[gi].rotate || a.rot == 0) rows(Const<false>{}, Const<false>{});
         else if (a.rot == a.d) rows(Const<true>{}, Const<true>{});
         else rows(Const<true>{}, Const<false>{});
+    }
+}
+
+// The half layout of bf16 rows: an item is 8 neighbours, and the other halves of its
+// pairs are an item of another lane of the warp and come from there. Rows are then
+// read and written whole, 256 bytes at a time at d = 128: 10.9 us for the queries of a
+// chunk, 13.7 us in two times 8 bytes a thread (float32, two times 16 bytes: 17.5 us so,
+// 21.5 us exchanged). Each lane of such a couple forms four of their eight angles.
+// A warp stays together for the exchange: who has no row only takes part in that.
+template <int U>
+__global__ void __launch_bounds__(RT, 4)
+    rope_half_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
+    using T = __nv_bfloat16;
+    const int l = threadIdx.x & ((1 << lanes_log2) - 1);
+    const long long t =
+        static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
+    const bool real = t < a.tokens && 8 * l < a.d;
+    const int b = real ? static_cast<int>(t) / a.N : 0, n = real ? static_cast<int>(t) - b * a.N : 0;
+    const int h0 = blockIdx.y * rows_per_y, h1 = h0 + rows_per_y;
+    const long long slot = real ? token_slot(a, t, blockIdx.y == 0 && l == 0) : -1;
+
+    const bool turned = l < a.rot >> 3;
+    const int half = a.rot >> 4;  // items of half the rotated part
+    const bool first = l < half;
+    const int lane = threadIdx.x & 31;
+    const int other = !turned ? lane : first ? lane + half : lane - half;
+    float c[8], s[8];  // s with the sign of the other half's share
+    if (h0 < a.rotated_rows) {
+        float cs[4] = {}, sn[4] = {};
+        if (real && turned) {
+            const int32_t* pos = a.pos + b * a.pos_batch + n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pair = first ? 8 * l + i : 8 * (l - half) + 4 + i;
+                turn(a.freqs[pair], axis_pos(a, pos, pair), a.mscale, a.sign, cs[i], sn[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float oc = __shfl_sync(~0u, cs[i], other), os = __shfl_sync(~0u, sn[i], other);
+            c[i] = first ? cs[i] : oc, c[4 + i] = first ? oc : cs[i];
+            s[i] = first ? -sn[i] : os, s[4 + i] = first ? -os : sn[i];
+        }
+    }
+
+    for (int gi = 0; gi < a.groups; ++gi) {
+        int lo, hi;
+        cut(a, gi, h0, h1, lo, hi);
+        if (lo >= hi) continue;
+        const Rows<T, T> r(a, a.g[gi], b, n, slot);
+        const bool live = real && r.live;
+        const T* x = r.x + 8 * l;
+        T* y = r.y + 8 * l;
+        const bool rotate = a.g[gi].rotate;
+        for (int h = lo; h < hi; h += U) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (live && h + u < hi) v[u] = *reinterpret_cast<const uint4*>(x + (h + u) * r.xh);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (rotate) {
+                    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                    uint32_t q[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q[i] = __shfl_sync(~0u, w[i], other);
+                    if (turned) {
+                        float f[8], g[8];
+                        unpack(w, f);
+                        unpack(q, g);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = f[i] * c[i] + g[i] * s[i];
+                        v[u] = make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]),
+                                          bf2(f[6], f[7]));
+                    }
+                }
+                if (live && h + u < hi) *reinterpret_cast<uint4*>(y + (h + u) * r.yh) = v[u];
+            }
+        }
     }
 }
 
@@ -266,31 +350,33 @@ __global__ void __launch_bounds__(RT)
 template <typename TI, typename TO>
 int launch(const RopeArgs& a, bool vec, cudaStream_t st) {
     // lanes of a token: one per item
-    const int need = a.half_style ? (a.d + 15) / 16 : a.d / 8;
     int lanes_log2 = 5;
-    vec = vec && need <= RT;
+    vec = vec && a.d / 8 <= RT;
     if (vec)
-        for (lanes_log2 = 0; (1 << lanes_log2) < need; ++lanes_log2) {}
+        for (lanes_log2 = 0; (1 << lanes_log2) < a.d / 8; ++lanes_log2) {}
     const long long per_cta = RT >> lanes_log2;
     const long long gx = (a.tokens + per_cta - 1) / per_cta;
     if (gx >= (1ll << 31)) return VELOX_EINVAL;
     // The heads are split until there are two CTAs per SM, and no further than four heads
     // a thread, since each part forms its angles again. Queries of a chunk (24 heads of
-    // 4608 tokens, bf16): 9.3 us so, 10.9 us with four CTAs per SM; 48 heads of
-    // 1000 tokens in the half layout 6.3 and 8.6 us; 200 tokens 3.9 us, 4.4 us down to one head
+    // 4608 tokens, bf16): 9.3 us so, 10.9 us with four CTAs per SM; 200 tokens of 72
+    // heads 3.9 us, 4.9 us split to two heads
     const long long want = std::max<long long>(1, (296 + gx - 1) / gx);
     const int parts = static_cast<int>(std::min<long long>({want, (a.rows + 3) / 4, 65535}));
     const int rows_per_y = (a.rows + parts - 1) / parts;
     const dim3 grid(static_cast<unsigned>(gx), (a.rows + rows_per_y - 1) / rows_per_y);
-    // rows loaded at once: 128 bytes of a thread (in the half layout and float32 the
-    // registers of 64 are what fits)
-    constexpr bool F = sizeof(TI) == 4;
+    constexpr bool BF = sizeof(TI) == 2;
+    constexpr int U = BF ? 8 : 4;  // rows at once: 128 bytes of a thread
+    // in the half layout an item's other half is a whole item, in the same warp
+    const bool exchange = BF && a.rot > 0 && a.rot % 16 == 0 && a.d <= 256;
     if (!vec)
         rope_scalar_kernel<TI, TO><<<grid, RT, 0, st>>>(a, rows_per_y);
-    else if (a.half_style)
-        rope_vec_kernel<TI, TO, true, F ? 1 : 4><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
+    else if (!a.half_style)
+        rope_vec_kernel<TI, TO, false, U><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
+    else if (exchange)
+        rope_half_kernel<4><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
     else
-        rope_vec_kernel<TI, TO, false, F ? 4 : 8><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
+        rope_vec_kernel<TI, TO, true, U><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
     return cudaGetLastError() == cudaSuccess ? VELOX_OK : VELOX_ECUDA;
 }
 
