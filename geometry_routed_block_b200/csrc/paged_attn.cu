@@ -22,6 +22,8 @@
 //     warp until its share is done. Then the CTA joins the parts of rows that its
 //     warps share, through shared memory; what reaches beyond the CTA (two rows
 //     at most) goes as (m, l, o) to the workspace, and a second kernel joins that.
+//   - Rows of a single request are all of one length: there a cluster of CTAs takes a
+//     row, and joins it through distributed shared memory, in one launch.
 //   - S = Q K^T has the query heads in rows 0-7 (and heads 8-15 in rows 8-15, when
 //     more than 8 share a key head). P is split into two bf16, P = hi + lo, with
 //     hi in rows 0-7 and lo in rows 8-15 of one product with V: the rows that 8
@@ -44,7 +46,11 @@ namespace {
 constexpr int UNIT = 16;       // tokens per unit: the smallest page
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
-constexpr int MAX_GRID = 320;  // CTAs at most (two per SM)
+constexpr int MAX_GRID = 320;  // CTAs at most
+// Bytes that the GPU's CTAs keep in flight at full occupancy. More is slower, DRAM then
+// serves too many places at once: the whole history of 24 heads (2.77 GB) takes 411 us at
+// 12 MB, 399 at 17, 409 at 19, 411 at 21, 422 at 28; a ragged batch 91.9, 88.6, 90.4, 94.6, 92.3
+constexpr double IN_FLIGHT = 17.5e6;
 constexpr int JT = 256;        // threads of the joining kernel
 constexpr int JW = JT / 32;
 constexpr int PPL = (MAX_GRID + JT - 1) / JT;  // parts that a lane looks after
@@ -281,6 +287,113 @@ __device__ __forceinline__ void empty_rows(const PagedAttnArgs& a, int r, int st
     }
 }
 
+// Four columns of a query head are an item of the CTA's join; a thread's items go side by
+// side.
+template <int D, int MT>
+struct Joined {
+    static constexpr int ITEMS = Cfg<D, MT>::HEADS * (D / 4) / NT;
+    static constexpr int HSTEP = NT / (D / 4);
+    static_assert(Cfg<D, MT>::HEADS * (D / 4) % NT == 0, "items of a thread");
+    float top[ITEMS], sum[ITEMS];
+    float4 acc[ITEMS];
+    __device__ __forceinline__ int head(int k) const { return threadIdx.x / (D / 4) + k * HSTEP; }
+    __device__ __forceinline__ int col() const { return 4 * (threadIdx.x % (D / 4)); }
+};
+
+__device__ __forceinline__ void add_scaled(float4& acc, float x, const float4& v) {
+    acc.x += x * v.x, acc.y += x * v.y, acc.z += x * v.z, acc.w += x * v.w;
+}
+__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// joins the entries `these` (bits) of the CTA's warps
+template <int D, int MT>
+__device__ __forceinline__ void join_entries(uint8_t* smem, uint32_t these, Joined<D, MT>& j) {
+    using C = Cfg<D, MT>;
+    const float* sm_m = reinterpret_cast<const float*>(smem + C::OFF_M) + j.head(0);
+    const float* sm_l = reinterpret_cast<const float*>(smem + C::OFF_L) + j.head(0);
+#pragma unroll
+    for (int k = 0; k < j.ITEMS; ++k) {
+        j.top[k] = -INFINITY, j.sum[k] = 0.0f;
+        j.acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (uint32_t es = these; es; es &= es - 1) {
+        const float* m = sm_m + (__ffs(es) - 1) * C::HEADS;
+#pragma unroll
+        for (int k = 0; k < j.ITEMS; ++k) j.top[k] = fmaxf(j.top[k], m[k * j.HSTEP]);
+    }
+    for (uint32_t es = these; es; es &= es - 1) {
+        const int e = __ffs(es) - 1;
+        const float* src = part_o<D, MT>(smem, e) + j.head(0) * D + j.col();
+#pragma unroll
+        for (int k = 0; k < j.ITEMS; ++k) {
+            const float x = ex2_approx(sm_m[e * C::HEADS + k * j.HSTEP] - finite_ref(j.top[k]));
+            j.sum[k] += x * sm_l[e * C::HEADS + k * j.HSTEP];
+            add_scaled(j.acc[k], x, *reinterpret_cast<const float4*>(src + k * j.HSTEP * D));
+        }
+    }
+}
+
+// a finished query head's four columns (and its lse with the first)
+template <int D>
+__device__ __forceinline__ void store_head(const PagedAttnArgs& a, long long row, int col,
+                                           const float4& acc, float top, float sum) {
+    const float inv = 1.0f / sum;
+    *reinterpret_cast<uint2*>(a.o + row * D + col) = make_uint2(
+        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && col == 0) a.lse[row] = log_sum(top, sum);
+}
+
+__device__ __forceinline__ float peer_f(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// The row of a cluster: every CTA joins its warps' parts, then each takes some of the
+// heads' columns and reads the others' results from their shared memory.
+template <int D, int MT>
+__device__ __forceinline__ void join_cluster(const PagedAttnArgs& a, uint8_t* smem, const Row& p,
+                                             uint32_t entries) {
+    using C = Cfg<D, MT>;
+    Joined<D, MT> j;
+    join_entries<D, MT>(smem, entries, j);
+    float* o = part_o<D, MT>(smem, 0);  // free: the parts lie in the rings
+    float* stats = reinterpret_cast<float*>(smem + C::OFF_SH);  // maxima, sums
+#pragma unroll
+    for (int k = 0; k < j.ITEMS; ++k) {
+        *reinterpret_cast<float4*>(o + j.head(k) * D + j.col()) = j.acc[k];
+        if (j.col() == 0) stats[j.head(k)] = j.top[k], stats[C::HEADS + j.head(k)] = j.sum[k];
+    }
+    cluster_sync();
+    const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
+    const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
+    const long long q_row = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
+    const int n = a.whole_rows;
+    for (int i = cluster_ctarank() * NT + threadIdx.x; i < heads * (D / 4); i += n * NT) {
+        const int h = i / (D / 4), col = 4 * (i % (D / 4));
+        const uint32_t so = smem_u32(o + h * D + col), sm = smem_u32(stats + h);
+        float top = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = 0; c < n; ++c) top = fmaxf(top, peer_f(map_to_rank(sm, c)));
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const float x = ex2_approx(peer_f(map_to_rank(sm, c)) - finite_ref(top));
+            sum += x * peer_f(map_to_rank(sm + 4 * C::HEADS, c));
+            add_scaled(acc, x, peer_f4(map_to_rank(so, c)));
+        }
+        store_head<D>(a, q_row + h, col, acc, top, sum);
+    }
+    cluster_sync();  // the others have read this CTA's shared memory
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(NT, 2)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -313,18 +426,21 @@ __global__ void __launch_bounds__(NT, 2)
     long long g0, g1;  // this warp's share: units g0 .. g1 - 1
     Row p;
     if (a.whole_rows) {
-        // one row per CTA, a quarter of it per warp
+        // a row per CTA or cluster, an equal part of it per warp
+        const int row = cta / a.whole_rows, piece = (cta - row * a.whole_rows) * NW + warp;
         p.base = 0;
-        p.r = cta / rows;
-        p.row = cta - p.r * rows;
+        p.r = row / rows;
+        p.row = row - p.r * rows;
         const int n = a.lens[p.r];
         p.n = clamp_len(n, cap);
         p.units = units_of(p.n);
         if (p.row == 0 && threadIdx.x == 0 && n != p.n && a.status)
             atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
-        g0 = p.units * warp / NW, g1 = p.units * (warp + 1) / NW;
+        const int pieces = a.whole_rows * NW;
+        g0 = static_cast<long long>(p.units) * piece / pieces;
+        g1 = static_cast<long long>(p.units) * (piece + 1) / pieces;
         __syncthreads();  // barriers initialised
-        if (p.n == 0 && p.row == 0) empty_rows<D>(a, p.r, a.R, cap);
+        if (p.n == 0 && p.row == 0 && piece < NW) empty_rows<D>(a, p.r, a.R, cap);
         if (p.n == 0) return;
     } else {
         const Work work = locate<NT>(a, cta * NW, NW, 1, sh, cta == 0);
@@ -389,7 +505,7 @@ __global__ void __launch_bounds__(NT, 2)
         settle();
     };
     int ahead = 0;  // units fetched and not yet used
-    for (int s = 0; s < C::ST; ++s)
+    for (int s = 0; s < a.stages; ++s)
         if (more) {
             fetch(s);
             ++ahead;
@@ -400,6 +516,7 @@ __global__ void __launch_bounds__(NT, 2)
     const int g = lane >> 2, t = lane & 3;
     int* ent = reinterpret_cast<int*>(smem + C::OFF_ENT) + 8 * warp;  // this warp's two parts
     if (lane < 2) ent[4 * lane] = -1;  // none yet
+    const bool clustered = a.whole_rows > 1;
     int slot = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -518,7 +635,7 @@ __global__ void __launch_bounds__(NT, 2)
                     fetch(slot);
                     ++ahead;
                 }
-                if (++slot == C::ST) slot = 0, parity ^= 1;
+                if (++slot == a.stages) slot = 0, parity ^= 1;
             }
             if (!ok) break;
 #pragma unroll
@@ -532,7 +649,7 @@ __global__ void __launch_bounds__(NT, 2)
                 }
             }
             const bool begins = u0 == 0, ends = u1 == p.units;
-            if (begins && ends) {
+            if (begins && ends && !clustered) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
                     if (8 * i + g < heads) {
@@ -546,9 +663,9 @@ __global__ void __launch_bounds__(NT, 2)
                     }
             } else {
                 // part 0: the end of a row that another warp began; part 1: a row that
-                // goes on in the next warp. Part 1 is this warp's last row, so its ring
-                // has no load in flight
-                const int e = 2 * warp + (ends ? 0 : 1);
+                // goes on in the next warp (or any part of a cluster's row). Part 1 is this
+                // warp's last row, so its ring has no load in flight
+                const int k = ends && !clustered ? 0 : 1, e = 2 * warp + k;
                 float* sm_o = part_o<D, MT>(smem, e);
                 float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M) + e * C::HEADS;
                 float* sm_l = reinterpret_cast<float*>(smem + C::OFF_L) + e * C::HEADS;
@@ -562,7 +679,7 @@ __global__ void __launch_bounds__(NT, 2)
                                 make_float2(o[i][j][0], o[i][j][1]);
                 }
                 if (lane == 0) {
-                    int* mine = ent + (ends ? 0 : 4);
+                    int* mine = ent + 4 * k;
                     mine[1] = p.r;
                     mine[2] = p.row;
                     mine[3] = begins;
@@ -579,7 +696,7 @@ __global__ void __launch_bounds__(NT, 2)
         volatile int never = 0;
         for (; ahead > 0; --ahead) {
             if (!mbar_wait(bars + 8 * slot, parity, &never, a.wait_ns)) break;
-            if (++slot == C::ST) slot = 0, parity ^= 1;
+            if (++slot == a.stages) slot = 0, parity ^= 1;
         }
     }
 
@@ -588,11 +705,13 @@ __global__ void __launch_bounds__(NT, 2)
     // in this CTA
     __syncthreads();
     const int* ents = reinterpret_cast<const int*>(smem + C::OFF_ENT);
-    const float* sm_m = reinterpret_cast<const float*>(smem + C::OFF_M);
-    const float* sm_l = reinterpret_cast<const float*>(smem + C::OFF_L);
     uint32_t left = 0;  // bit e: an entry
 #pragma unroll
     for (int e = 0; e < 2 * NW; ++e) left |= (ents[4 * e] >= 0 ? 1u : 0u) << e;
+    if (clustered) {
+        join_cluster<D, MT>(a, smem, p, left);
+        return;
+    }
     while (left) {
         const int e0 = __ffs(left) - 1;
         const uint32_t enders = left & 0x55555555u;
@@ -605,50 +724,19 @@ __global__ void __launch_bounds__(NT, 2)
         const long long q_row =
             static_cast<long long>(r) * a.H + hk * a.group + ht * a.tile_heads;
         float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
-        // four columns of a head are an item; a thread's items go side by side
-        constexpr int ITEMS = C::HEADS * (D / 4) / NT;
-        static_assert(C::HEADS * (D / 4) % NT == 0, "items of a thread");
-        const int col = 4 * (threadIdx.x % (D / 4)), h0 = threadIdx.x / (D / 4);
-        constexpr int HSTEP = NT / (D / 4);  // item k: head h0 + k HSTEP
-        float top[ITEMS], sum[ITEMS];
-        float4 acc[ITEMS];
+        Joined<D, MT> j;
+        join_entries<D, MT>(smem, these, j);
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            top[k] = -INFINITY, sum[k] = 0.0f;
-            acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        for (uint32_t es = these; es; es &= es - 1) {
-            const float* m = sm_m + (__ffs(es) - 1) * C::HEADS + h0;
-#pragma unroll
-            for (int k = 0; k < ITEMS; ++k) top[k] = fmaxf(top[k], m[k * HSTEP]);
-        }
-        for (uint32_t es = these; es; es &= es - 1) {
-            const int e = __ffs(es) - 1;
-            const float* src = part_o<D, MT>(smem, e) + h0 * D + col;
-#pragma unroll
-            for (int k = 0; k < ITEMS; ++k) {
-                const float x = ex2_approx(sm_m[e * C::HEADS + h0 + k * HSTEP] -
-                                           (top[k] == -INFINITY ? 0.0f : top[k]));
-                const float4 v = *reinterpret_cast<const float4*>(src + k * HSTEP * D);
-                sum[k] += x * sm_l[e * C::HEADS + h0 + k * HSTEP];
-                acc[k].x += x * v.x, acc[k].y += x * v.y, acc[k].z += x * v.z, acc[k].w += x * v.w;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int h = h0 + k * HSTEP;
+        for (int k = 0; k < j.ITEMS; ++k) {
+            const int h = j.head(k), col = j.col();
             if (h >= heads) break;
             if (begins && ends) {
-                const float inv = 1.0f / sum[k];
-                *reinterpret_cast<uint2*>(a.o + (q_row + h) * D + col) =
-                    make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv),
-                               pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
-                if (a.lse && col == 0) a.lse[q_row + h] = log_sum(top[k], sum[k]);
+                store_head<D>(a, q_row + h, col, j.acc[k], j.top[k], j.sum[k]);
             } else {
-                *reinterpret_cast<float4*>(part + h * D + col) = acc[k];
+                *reinterpret_cast<float4*>(part + h * D + col) = j.acc[k];
                 if (col == 0) {
-                    part[C::HEADS * D + h] = top[k];
-                    part[C::HEADS * D + C::HEADS + h] = sum[k];
+                    part[C::HEADS * D + h] = j.top[k];
+                    part[C::HEADS * D + C::HEADS + h] = j.sum[k];
                 }
             }
         }
@@ -794,6 +882,20 @@ __global__ void __launch_bounds__(JT)
     }
 }
 
+// CTAs per row where rows are not dealt out by length, else 0: one for short histories;
+// a cluster for a single request, whose rows are all of one length, where clusters of 8
+// or 16 make up a grid that fills the GPU. 24 key heads, one launch and no workspace
+// against two: 700 tokens 7.5 and 9.9 us, 4096 tokens 15.2 and 18.1 us, 225,793 tokens 392 and
+// 399 us; 8 key heads (128 CTAs, not taken) 9.9 and 12.0 us at 4096 tokens, 195 and 148 us
+// at 225,793.
+int ctas_per_row(const PagedAttnArgs& a, long long rows) {
+    if (a.whole_rows) return 1;
+    if (a.R > 1) return 0;
+    for (int n = 16; n >= 8; n /= 2)
+        if (rows * n <= 256 && rows * n >= 160) return n;
+    return 0;
+}
+
 template <int D, int MT>
 int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream_t st) {
     using C = Cfg<D, MT>;
@@ -807,26 +909,42 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return VELOX_ECUDA;
-    const int resident = std::min(2 * sms, MAX_GRID);
+    const int resident = std::min(7 * sms / 4, MAX_GRID);
     const long long rows = static_cast<long long>(a.R) * a.Hkv * a.head_tiles;
     const long long units = static_cast<long long>(a.max_pages) * a.page / UNIT;
+    a.whole_rows = ctas_per_row(a, rows);
     // no more CTAs than the longest histories could keep busy
     a.grid = static_cast<int>(
-        a.whole_rows ? rows
+        a.whole_rows ? rows * a.whole_rows
                      : std::min<long long>(resident, (rows * (units + ROW_COST) + NW * MIN_SHARE - 1) /
                                                          (NW * MIN_SHARE)));
+    // units in flight: as many as come nearest to IN_FLIGHT bytes on the whole GPU
+    const double per_stage = static_cast<double>(a.grid) * NW * C::STAGE;
+    a.stages = std::max(2, std::min(C::ST, static_cast<int>(IN_FLIGHT / per_stage + 0.5)));
     auto kern = paged_attn_kernel<D, MT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
         return VELOX_ECUDA;
-    kern<<<a.grid, NT, C::SMEM, st>>>(tk, tv, a);
-    if (cudaGetLastError() != cudaSuccess) return VELOX_ECUDA;
-    if (a.whole_rows || a.grid == 1) return VELOX_OK;  // no row is shared
+    if (a.whole_rows > 8 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return VELOX_ECUDA;
+    cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(JT);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    if (a.whole_rows > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = a.whole_rows;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&cfg, kern, tk, tv, a) != cudaSuccess) return VELOX_ECUDA;
+    if (a.whole_rows || a.grid == 1) return VELOX_OK;  // no row is shared between shares
+    cfg.blockDim = dim3(JT);
+    cfg.dynamicSmemBytes = 0;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;

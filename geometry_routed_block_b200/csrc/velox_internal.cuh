@@ -126,7 +126,8 @@ struct PagedAttnArgs {
     int tile_heads;  // query heads per tile
     int grid;        // CTAs that share the work
     int page_shift;  // log2(page)
-    int whole_rows;  // a CTA per row
+    int stages;      // units that a warp keeps in flight
+    int whole_rows;  // CTAs per row where rows are not dealt out by length, else 0
     float scale_log2;
     __nv_bfloat16* o;
     float* lse;

@@ -487,6 +487,38 @@ def test_attn_matches_oracle(vx, case):
     check_attn(o3, l3, to.token_attention(host(q), host(kp), host(vp), table, lens, 0.9), lens, 0.9, d)
 
 
+@pytest.mark.parametrize("H,Hkv,d", [(24, 24, 128), (12, 12, 64), (32, 32, 64), (40, 10, 128), (160, 10, 128),
+                                     (170, 10, 64)])
+@pytest.mark.parametrize("n", [0, 1, 16, 17, 130, 1000, 3001])
+def test_attn_of_one_request_by_clusters(vx, H, Hkv, d, n):
+    """One request whose key heads (and tiles of query heads) make up a grid of clusters, from no
+    token to more than every warp has units; the table is always wide."""
+    page = 64
+    kp, vp, table, num = attn_state(1, Hkv, d, page, [n], seed=H + n)
+    table = np.concatenate([table, np.full((1, 60), -1)], 1)
+    q = torch.randn(1, H, d, device="cuda").to(torch.bfloat16)
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    want = to.token_attention(host(q), host(kp), host(vp), table, [n])
+    o, lse = vx.paged_attn(q, kp, vp, i32(table), i32([n]), status=status)
+    assert flags(vx, status) == 0
+    check_attn(o, lse, want, [n], 1 / math.sqrt(d), d)
+    o2, _ = vx.paged_attn(q, kp, vp, i32(table), i32([n]))
+    assert torch.equal(o, o2)
+    # as one of two requests the rows are dealt out by length: the same up to rounding
+    two = torch.cat([q, q])
+    o3, l3 = vx.paged_attn(two, kp, vp, i32(np.repeat(table, 2, 0)), i32([n, n]))
+    for r in range(2):
+        check_attn(o3[r:r + 1], l3[r:r + 1], want, [n], 1 / math.sqrt(d), d)
+    if n == 130:
+        t = table.copy()
+        t[0, 1] = num
+        vx.paged_attn(q, kp, vp, i32(t), i32([n]), status=status)
+        assert flags(vx, status) == vx.VELOX_STATUS_BAD_INDEX
+        o, lse = vx.paged_attn(q, kp, vp, i32(np.where(table < 0, 0, table)), i32([-3]), status=status)
+        assert flags(vx, status) == vx.VELOX_STATUS_BAD_INDEX
+        assert (o == 0).all() and torch.isneginf(lse).all()
+
+
 def test_attn_extreme_scores_and_values(vx):
     """A last key that dwarfs all before it, scores of -inf, an infinite value among the valid."""
     d, page, n = 128, 16, 300
