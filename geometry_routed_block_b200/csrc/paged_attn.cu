@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "attn_common.cuh"
 
@@ -47,9 +48,10 @@ constexpr int UNIT = 16;       // tokens per unit: the smallest page
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most
-// Bytes that the GPU's CTAs keep in flight at full occupancy. More is slower, DRAM then
-// serves too many places at once: the whole history of 24 heads (2.77 GB) takes 411 us at
-// 12 MB, 399 at 17, 409 at 19, 411 at 21, 422 at 28; a ragged batch 91.9, 88.6, 90.4, 94.6, 92.3
+// Bytes that the CTAs together keep in flight. More is slower, DRAM then serves too many
+// places at once: the whole history of 24 heads (2.77 GB) takes 411 us at 12 MB, 399 at 17,
+// 409 at 19, 411 at 21, 422 at 28 (in a steady loop, under the power cap, 406 at 17 and
+// 438 at 28); a ragged batch 91.9, 88.6, 90.4, 94.6, 92.3
 constexpr double IN_FLIGHT = 17.5e6;
 constexpr int JT = 256;        // threads of the joining kernel
 constexpr int JW = JT / 32;
@@ -883,15 +885,16 @@ __global__ void __launch_bounds__(JT)
 }
 
 // CTAs per row where rows are not dealt out by length, else 0: one for short histories;
-// a cluster for a single request, whose rows are all of one length, where clusters of 8
-// or 16 make up a grid that fills the GPU. 24 key heads, one launch and no workspace
-// against two: 700 tokens 7.5 and 9.9 us, 4096 tokens 15.2 and 18.1 us, 225,793 tokens 392 and
-// 399 us; 8 key heads (128 CTAs, not taken) 9.9 and 12.0 us at 4096 tokens, 195 and 148 us
-// at 225,793.
+// a cluster for a single request, whose rows are all of one length, where clusters of 16,
+// 10 or 8 (sizes that the GPU holds at once, with two CTAs per SM) make up a grid that
+// fills it. 24 key heads, one launch and no workspace against two, in a steady loop: 4096
+// tokens 16.7 and 19.8 us, 32,768 tokens 67.7 and 70.3 us, 225,793 tokens 412 and 407 us
+// (clusters of 8: 16.4, 70.3, 455 us; of 11, which do not fit: 26.2, 103, 610 us). 8 key
+// heads (128 CTAs, not taken): 9.9 and 12.0 us at 4096 tokens, 195 and 148 us at 225,793.
 int ctas_per_row(const PagedAttnArgs& a, long long rows) {
     if (a.whole_rows) return 1;
     if (a.R > 1) return 0;
-    for (int n = 16; n >= 8; n /= 2)
+    for (const int n : {16, 10, 8})
         if (rows * n <= 256 && rows * n >= 160) return n;
     return 0;
 }
