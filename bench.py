@@ -1,7 +1,8 @@
 """Benchmark of the Velox geometry-routed attention path on B200.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
-                    [--workload headline|sweep|pipeline|robustness|rollout|overlap] [--P 48]
+                    [--workload headline|sweep|pipeline|robustness|rollout|overlap|tokens]
+                    [--P 48]
 
 One step = one pass of the whole hot path over one chunk's synthetic inputs,
 with the KV cache resident in HBM: frustum slices of every past chunk, slice
@@ -43,6 +44,12 @@ built at each chunk boundary or pipelined one chunk ahead.
 --workload overlap times the slice-overlap kernel at the headline size and on a
 stress shape (64 scenes at 256 x 384 against 96 slices) against a measured
 float64 FMA rate.
+
+--workload tokens decodes single tokens of one rollout against its whole
+history (--P past chunks and the current one) held in a paged cache: per step
+the plan of the new token's page and slot, and in each of --layers layers the
+append (rotary positions, key and value into their slot) and the attention of the
+token over all pages; the step is captured into a CUDA graph and replayed.
 """
 from __future__ import annotations
 
@@ -1404,6 +1411,72 @@ def run_overlap(args):
     print(json.dumps(out), flush=True)
 
 
+def run_tokens(args):
+    """Single tokens of one rollout against its whole history in a paged cache
+    (PagedCache): plan, then append and attention in every layer, one CUDA graph
+    per step. The history is appended chunk by chunk through the same calls."""
+    import torch
+    from geometry_routed_block_b200 import velox as vx
+    from geometry_routed_block_b200.paged import PagedCache
+    if int(os.environ.get("RANK", "0")) != 0:
+        return
+    local = int(os.environ.get("LOCAL_RANK", "0"))
+    torch.cuda.set_device(local)
+    device = torch.device("cuda", local)
+    s = synth.shape_for(3)
+    P, L, H, d, page = args.P or 48, args.layers, s.H, s.d, 128
+    steps = max(3, min(args.steps, 200))
+    warm = max(3, args.warmup)
+    history = (P + 1) * s.Nq
+    pages = -(-(history + steps + warm + 2) // page)
+    freqs, _ = vx.rope_freqs(d, device=device)
+    c = PagedCache(L, 1, H, d, page, pages, pages, freqs=freqs, device=device)
+    g = torch.Generator(device=device).manual_seed(1012)
+    draw = lambda n: torch.randn((n, H, d), generator=g, device=device).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device=device)
+    add = torch.full((1,), s.Nq, **i32)
+    chunk_plan = c.new_plan(s.Nq)
+    k, v = draw(s.Nq), draw(s.Nq)
+    for _ in range(P + 1):
+        c.plan(add, s.Nq, out=chunk_plan)
+        for layer in range(L):
+            c.append(layer, chunk_plan, k, v)
+    one, plan = torch.ones(1, **i32), c.new_plan(1)
+    qkv = [(draw(1), draw(1), draw(1)) for _ in range(L)]
+    q_rot, o = torch.empty_like(qkv[0][0]), torch.empty_like(qkv[0][0])
+
+    def step():
+        c.plan(one, 1, out=plan)
+        for layer, (q, k1, v1) in enumerate(qkv):
+            c.append(layer, plan, k1, v1, q=q, out=q_rot)
+            c.attend(layer, q_rot, out=o)
+
+    side = torch.cuda.Stream(device=device)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(warm):
+        graph.replay()
+    t = time_loop(torch, graph.replay, steps)
+    c.check()
+    tokens = int(c.lens.item())
+    kv_bytes = 4.0 * L * H * d * tokens  # K and V in bf16, once per step
+    hbm = load_peaks()[0]["hbm_gbs"]
+    achieved = kv_bytes / (t * 1e-3) / 1e9
+    print(json.dumps({
+        "workload": f"one token against {tokens} cached tokens, {L} layers x {H} heads x d {d}, pages of "
+                    f"{page}: plan, append and attention per step in a CUDA graph",
+        "data": "synthetic", "n_gpus": 1, "steps": steps, "ms_per_token": round(t, 4),
+        "us_per_layer": round(1e3 * t / L, 2), "kv_bytes_per_token": kv_bytes,
+        "roofline": {"bound": "hbm", "achieved": round(achieved, 1), "peak": hbm, "unit": "GB/s",
+                     "frac": round(achieved / hbm, 4)},
+    }), flush=True)
+
+
 def run_reference(args):
     """The reference arm: the fp64 CPU oracle (the method's pages publish no
     code) on the host cores. Each step is one bounded sample of the workload
@@ -1455,7 +1528,8 @@ def main():
     ap.add_argument("--warmup", type=int, default=5)
     ap.add_argument("--impl", default="velox", choices=["velox", "reference"])
     ap.add_argument("--workload", default="headline",
-                    choices=["headline", "sweep", "pipeline", "robustness", "rollout", "overlap"])
+                    choices=["headline", "sweep", "pipeline", "robustness", "rollout", "overlap",
+                             "tokens"])
     ap.add_argument("--chunks", type=int, default=4, help="chunks (rollout workload)")
     ap.add_argument("--denoise-steps", type=int, default=4, help="steps per chunk (rollout)")
     ap.add_argument("--layers", type=int, default=30, help="layers (pipeline workload)")
@@ -1480,6 +1554,8 @@ def main():
         run_rollout(args)
     elif args.workload == "overlap":
         run_overlap(args)
+    elif args.workload == "tokens":
+        run_tokens(args)
     else:
         run_gpu(args)
 
