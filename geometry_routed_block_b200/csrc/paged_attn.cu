@@ -72,8 +72,7 @@ struct Cfg {
     static constexpr int HALF = UNIT * 128;        // 16 tokens x 64 columns
     static constexpr int TILE = UNIT * D * 2;      // K or V of a unit
     static constexpr int STAGE = 2 * TILE;
-    // ring depth per warp: what two CTAs per SM have room for, 96 KB (64 KB with two
-    // tiles of parts) in flight
+    // units that a warp's ring has room for with two CTAs per SM (the launch may use fewer)
     static constexpr int ST = (D == 128 ? 3 : 6) - (MT == 2 ? (D == 128 ? 1 : 2) : 0);
     static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][HEADS][D]: a warp's first row
     static constexpr int OFF_M = OFF_O + NW * HEADS * D * 4;   // float [2 NW][HEADS]

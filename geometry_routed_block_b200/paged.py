@@ -14,7 +14,9 @@ the library calls:
 All state lives on the device and nothing is read back, so a step can be
 captured into a CUDA graph and replayed: lengths, table and free list carry on
 from replay to replay. What a call on the device cannot do (no page left, a
-length out of range) shows in `status`; `check()` reads it.
+length out of range) shows in `status`; `check()` reads it. The calls on one cache
+follow one another (one stream, or events between streams): they share its state
+and one workspace.
 
 Orchestration only: every step runs in libvelox's kernels.
 """

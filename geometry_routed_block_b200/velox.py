@@ -458,8 +458,8 @@ def _in_dtype(t: torch.Tensor, name: str) -> int:
 def _sections(style: str, sections: tuple):
     if style not in ROPE_STYLES:
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
-    if not 1 <= len(sections) <= 3:
-        raise ValueError("one to three position axes")
+    if not 1 <= len(sections) <= 3 or not all(0 <= n <= 2048 for n in sections):
+        raise ValueError("one to three position axes, of 0 to 2048 pairs each")
     return ROPE_STYLES[style], len(sections), (_c_int * 3)(*sections)
 
 
@@ -468,7 +468,7 @@ def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse
     if freqs.dim() != 1:
         raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
     n = freqs.shape[0]
-    code, axes, sec = _sections(style, (n,) if sections is None else tuple(sections))
+    code, axes, sec = _sections(style, (n,) if sections is None else tuple(map(int, sections)))
     return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, mscale,
                  1 if inverse else 0)
 

@@ -234,6 +234,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(vx):
         vx.rope(x, pos, fr, sections=(16, 16))      # two axes, positions of one
     with pytest.raises(ValueError):
         vx.rope(x, pos, fr, style="both")
+    for bad in ((), (8, 8, 8, 8), (-1, 33), (2**32 + 32,)):
+        with pytest.raises(ValueError):
+            vx.rope(x, pos, fr, sections=bad)
     with pytest.raises(ValueError, match="dense"):
         vx.rope(torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)[..., ::2], pos, fr)
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
