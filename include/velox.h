@@ -36,8 +36,8 @@
  *     all its calls share the library's scratch array, so they must not
  *     overlap on the GPU (serialise them, e.g. on one stream).
  *   - `status` arguments (may be NULL) point to one device int32 that kernels
- *     OR VELOX_STATUS_* bits into when they detect a bad index or give up a
- *     bounded wait; the caller zeroes it and reads it back.
+ *     OR VELOX_STATUS_* bits into when they detect a bad index, find no room or
+ *     give up a bounded wait; the caller zeroes it and reads it back.
  */
 #ifndef VELOX_H
 #define VELOX_H
