@@ -60,11 +60,12 @@ constexpr int ROW_COST = 2;    // empty units that a row counts for
 // units per warp at least: fewer would cost more joining than they save
 constexpr int MIN_SHARE = 2;
 
-// Where no row can be longer than this (by the width of the table) and there are no
-// more rows than CTAs fit on the GPU at once, a CTA takes a row, and nothing is joined.
-// Measured at 512 tokens: 8.7 to 10.2 us, split 8.4 to 9.3 us; at 64 tokens 4.1 and 8.3 us;
-// at 1024 tokens 13.3 and 8.5 us (one launch less on the host besides).
-constexpr int WHOLE_UNITS = 32, WHOLE_ROWS = 256;
+// Where no row can be longer (by the width of the table) than so many units for each of the
+// n = 1, 2, 4 or 8 CTAs that every row can have at once, rows are not dealt out by length:
+// a CTA or a cluster takes a row, in one launch and without a workspace. 32 / 8 heads, one
+// request: 20 tokens 4.8 us, 257 tokens 6.5 us (one CTA a row 8.4, dealt out 9.1), 480 tokens 6.7
+// us (10.6, 9.2); 1024 tokens with one CTA a row 16.4 us, dealt out 9.4.
+constexpr int WHOLE_UNITS = 32, WHOLE_CTAS = 256;
 
 template <int D, int MT>
 struct Cfg {
@@ -883,16 +884,15 @@ __global__ void __launch_bounds__(JT)
     }
 }
 
-// CTAs per row where rows are not dealt out by length, else 0: one for short histories;
-// a cluster for a single request, whose rows are all of one length, where clusters of 16,
+// CTAs per row where rows are not dealt out by length, else 0: those of a short history
+// (paged_attn_whole); a cluster for a single request, whose rows are all of one length, where clusters of 16,
 // 10 or 8 (sizes that the GPU holds at once, with two CTAs per SM) make up a grid that
 // fills it. 24 key heads, one launch and no workspace against two, in a steady loop: 4096
 // tokens 16.7 and 19.8 us, 32,768 tokens 67.7 and 70.3 us, 225,793 tokens 412 and 407 us
 // (clusters of 8: 16.4, 70.3, 455 us; of 11, which do not fit: 26.2, 103, 610 us). 8 key
 // heads (128 CTAs, not taken): 9.9 and 12.0 us at 4096 tokens, 195 and 148 us at 225,793.
 int ctas_per_row(const PagedAttnArgs& a, long long rows) {
-    if (a.whole_rows) return 1;
-    if (a.R > 1) return 0;
+    if (a.whole_rows || a.R > 1) return a.whole_rows;
     for (const int n : {16, 10, 8})
         if (rows * n <= 256 && rows * n >= 160) return n;
     return 0;
@@ -957,9 +957,14 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
 
 }  // namespace
 
-bool paged_attn_whole(int R, int H, int Hkv, int page, int max_pages) {
+int paged_attn_whole(int R, int H, int Hkv, int page, int max_pages) {
     const long long rows = static_cast<long long>(R) * Hkv * ((H / Hkv + 15) / 16);
-    return rows <= WHOLE_ROWS && static_cast<long long>(max_pages) * page / UNIT <= WHOLE_UNITS;
+    const long long units = static_cast<long long>(max_pages) * page / UNIT;
+    int n = 8;
+    while (n > 0 && rows * n > WHOLE_CTAS) n /= 2;
+    if (units > static_cast<long long>(WHOLE_UNITS) * n) return 0;
+    while (n > 1 && units < NW / 2 * n) n /= 2;  // a unit for every other warp
+    return n;
 }
 
 size_t paged_attn_ws_bytes(int R, int H, int Hkv, int d) {

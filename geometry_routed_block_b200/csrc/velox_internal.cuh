@@ -135,8 +135,9 @@ struct PagedAttnArgs {
     int32_t* status;
     unsigned long long wait_ns;
 };
-// whether a call is never split, and needs no workspace
-bool paged_attn_whole(int R, int H, int Hkv, int page, int max_pages);
+// CTAs per row where histories are so short that rows are not dealt out by length, and no
+// workspace is needed; else 0
+int paged_attn_whole(int R, int H, int Hkv, int page, int max_pages);
 size_t paged_attn_ws_bytes(int R, int H, int Hkv, int d);
 int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnArgs& a, int d,
                       cudaStream_t st);

@@ -682,6 +682,12 @@ def paged_attn_workspace(R: int, H: int, Hkv: int, d: int, device="cuda") -> tor
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _needs_no_workspace(rows: int, longest: int) -> bool:
+    """The header's rule for short histories of few rows."""
+    n = 8 if rows <= 32 else 4 if rows <= 64 else 2 if rows <= 128 else 1 if rows <= 256 else 0
+    return longest <= 512 * n
+
+
 def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                lens: torch.Tensor, scale: float | None = None, want_lse: bool = True,
                ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -709,8 +715,8 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
             return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status)
     if ws is not None:
         pw, nw = _arg(ws, "ws", torch.uint8, None, index), ws.numel()
-    elif width * page <= 512 and R * Hkv * ((H // max(Hkv, 1) + 15) // 16) <= 256:
-        pw, nw = None, 0  # not split: the call needs none
+    elif _needs_no_workspace(R * Hkv * ((H // max(Hkv, 1) + 15) // 16), width * page):
+        pw, nw = None, 0
     else:
         ws = paged_attn_workspace(R, H, Hkv, d, q.device)
         pw, nw = ws.data_ptr(), ws.numel()

@@ -489,8 +489,8 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  *   o [R][H][d] bf16 output, which shares nothing with q; lse [R][H] float32 output (natural log of the
  *   softmax denominator of the scaled scores) or NULL
  *   ws  scratch of velox_paged_attn_workspace_size bytes (256-B aligned); may be
- *       NULL (ws_bytes 0) for short histories of few rows, which are not split:
- *       max_pages * page <= 512 and R * Hkv * ceil(H / Hkv / 16) <= 256
+ *       NULL (ws_bytes 0) for short histories of few rows: where for an n of 1, 2, 4 or
+ *       8, max_pages * page <= 512 n and R * Hkv * ceil(H / Hkv / 16) * n <= 256
  * A request of length 0 gets zeros, with lse = -inf. What lies in a page behind the
  * last token may be anything, NaN too. Scores and softmax statistics are
  * float32; probabilities enter the tensor-core product as the sum of two bf16.

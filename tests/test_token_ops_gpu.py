@@ -470,11 +470,16 @@ ATTNS = [  # H, Hkv, d, page, lens
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["narrow", "wide"])
 @pytest.mark.parametrize("case", ATTNS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-R{len(c[4])}")
-def test_attn_matches_oracle(vx, case):
+def test_attn_matches_oracle(vx, case, wide):
+    """Narrow tables (short histories take a CTA or a cluster per row) and wide ones (rows are
+    dealt out by length)."""
     H, Hkv, d, page, lens = case
     R = len(lens)
     kp, vp, table, num = attn_state(R, Hkv, d, page, lens, seed=H * page + d)
+    if wide:
+        table = np.concatenate([table, np.full((R, 4200 // page + 1), -1)], 1)
     q = torch.randn(R, H, d, device="cuda").to(torch.bfloat16)
     status = torch.zeros(1, dtype=I32, device="cuda")
     want = to.token_attention(host(q), host(kp), host(vp), table, lens)
@@ -495,7 +500,7 @@ def test_attn_of_one_request_by_clusters(vx, H, Hkv, d, n):
     token to more than every warp has units; the table is always wide."""
     page = 64
     kp, vp, table, num = attn_state(1, Hkv, d, page, [n], seed=H + n)
-    table = np.concatenate([table, np.full((1, 60), -1)], 1)
+    table = np.concatenate([table, np.full((1, 200), -1)], 1)
     q = torch.randn(1, H, d, device="cuda").to(torch.bfloat16)
     status = torch.zeros(1, dtype=I32, device="cuda")
     want = to.token_attention(host(q), host(kp), host(vp), table, [n])
@@ -562,8 +567,8 @@ def test_attn_bad_pages_and_lengths_are_flagged(vx):
     kp, vp, table, num = attn_state(3, Hkv, d, page, lens, seed=9, garbage=False)
     q = torch.randn(3, H, d, device="cuda").to(torch.bfloat16)
     status = torch.zeros(1, dtype=I32, device="cuda")
-    for bad in (num, -1, 2 ** 31 - 1, -2 ** 31):
-        t = table.copy()
+    for bad, wide in ((num, 0), (-1, 300), (2 ** 31 - 1, 0), (-2 ** 31, 300)):
+        t = np.concatenate([table, np.full((3, wide), -1)], 1)
         t[1, 1] = bad
         o, lse = vx.paged_attn(q, kp, vp, i32(t), i32(lens), status=status)
         assert flags(vx, status) == vx.VELOX_STATUS_BAD_INDEX

@@ -148,7 +148,7 @@ def test_plan_and_release_reject(vx):
 
 def test_attn_rejects(vx):
     ok = dict(q=FAKE, kp=FAKE, vp=FAKE, table=FAKE, lens=FAKE, R=2, H=8, Hkv=2, d=64, page=16, np=32,
-              mp=80, scale=0.125, o=FAKE, lse=None, ws=FAKE, n=1 << 30)
+              mp=300, scale=0.125, o=FAKE, lse=None, ws=FAKE, n=1 << 30)
 
     def call(**kw):
         a = {**ok, **kw}
@@ -178,10 +178,13 @@ def test_attn_rejects(vx):
     rejects(call, -1, ws=ctypes.c_void_p((1 << 20) + 16))
     if not torch.cuda.is_available():
         assert call(n=need) == OK_PAST_CHECKS
-        assert call(mp=32, ws=None, n=0) == OK_PAST_CHECKS        # never split: no workspace
-        assert call(mp=32, R=128, ws=None, n=0) == OK_PAST_CHECKS
-    rejects(call, -1, mp=33, ws=None, n=0)
-    rejects(call, -1, mp=32, R=129, ws=None, n=0)
+        # short histories of few rows need no workspace: 512 tokens for each CTA a row can have
+        for R, mp in ((2, 256), (16, 256), (17, 128), (32, 128), (33, 64), (64, 64), (65, 32), (128, 32)):
+            assert call(mp=mp, R=R, ws=None, n=0) == OK_PAST_CHECKS
+    for R, mp in ((2, 257), (16, 257), (17, 129), (32, 129), (33, 65), (64, 65), (65, 33), (128, 33), (129, 1)):
+        rejects(call, -1, mp=mp, R=R, ws=None, n=0)
+        assert not vx._needs_no_workspace(R * 2, mp * 16)
+        assert vx._needs_no_workspace(R * 2, (mp - 1) * 16)
     rejects(call, -1, mp=4, page=128, R=8, H=40 * 17, Hkv=17, ws=None, n=0)  # three tiles of heads
     for bad in ((0, 8, 2, 64), (2, 7, 2, 64), (2, 8, 0, 64), (2, 8, 2, 96), (65536, 8, 2, 64)):
         assert vx.lib.velox_paged_attn_workspace_size(*bad) == 0
