@@ -384,8 +384,12 @@ int velox_rope(const void* x, int dtype, int B, int H, int N, int d, const int64
     const int esize = dtype == VELOX_BF16 ? 2 : 4;
     if (!aligned(x, esize) || !aligned(y, esize)) return VELOX_EINVAL;
     const int dims[3] = {B, H, N};
-    for (int i = 0; i < 3; ++i)
+    int64_t xd[3], yd[3];  // 0 along dimensions of size 1
+    for (int i = 0; i < 3; ++i) {
         if (xs[i] < 0 || ys[i] < 0 || (ys[i] == 0 && dims[i] > 1)) return VELOX_EINVAL;
+        xd[i] = dims[i] > 1 ? xs[i] : 0;
+        yd[i] = dims[i] > 1 ? ys[i] : 0;
+    }
 
     velox::RopeArgs r{};
     const int rc = set_rope(r, rope, d, pos);
@@ -403,10 +407,10 @@ int velox_rope(const void* x, int dtype, int B, int H, int N, int d, const int64
     g.y = y;
     g.heads = H;
     g.rotate = 1;
-    g.xb = xs[0], g.xh = xs[1], g.xn = xs[2];
-    g.yb = ys[0], g.yh = ys[1], g.yn = ys[2];
-    const bool vec = vec_rope(r) && vec_rows(x, esize, xs[0], xs[1], xs[2]) &&
-                     vec_rows(y, esize, ys[0], ys[1], ys[2]);
+    g.xb = xd[0], g.xh = xd[1], g.xn = xd[2];
+    g.yb = yd[0], g.yh = yd[1], g.yn = yd[2];
+    const bool vec = vec_rope(r) && vec_rows(x, esize, xd[0], xd[1], xd[2]) &&
+                     vec_rows(y, esize, yd[0], yd[1], yd[2]);
     return velox::rope_launch(r, dtype, false, vec, as_stream(stream));
 }
 
@@ -453,11 +457,11 @@ int velox_paged_append(const void* q, const void* k, const void* v, int dtype, i
         g.heads = heads;
         g.rotate = rotate;
         g.to_pages = to_pages;
-        g.xn = s[0], g.xh = s[1];
+        g.xn = N > 1 ? s[0] : 0, g.xh = heads > 1 ? s[1] : 0;
         g.yn = static_cast<long long>(heads) * d, g.yh = d;
         r.rows += heads;
         if (rotate) r.rotated_rows += heads;
-        vec = vec && vec_rows(x, esize, s[0], s[1], 0);
+        vec = vec && vec_rows(x, esize, g.xn, g.xh, 0);
     };
     const int rotate = r.rot > 0;
     if (q) add(q, qs, H, rotate, q_out, false);

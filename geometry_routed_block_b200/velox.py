@@ -370,6 +370,8 @@ def depth_multiwarp_noalloc(past_depth: torch.Tensor, past_cams: torch.Tensor,
 # Stream object (1.5 to 3 us each on the host of a B200).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+# pieces of an int32 buffer; no gradients run through them that would need views
+_pieces = torch.unsafe_split_with_sizes
 _I32, _F32, _BF16, _F64 = torch.int32, torch.float32, torch.bfloat16, torch.float64
 
 
@@ -410,12 +412,10 @@ def _int64s(values: tuple):
 
 
 def _rows(t: torch.Tensor, name: str) -> tuple:
-    """The strides of a tensor whose innermost dimension is dense, 0 along dimensions of size 1."""
-    shape, stride = t.shape, t.stride()
-    if stride[-1] != 1 and shape[-1] > 1:
+    """The strides of a tensor whose innermost dimension is dense."""
+    stride = t.stride()
+    if stride[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be dense in its last dimension")
-    if 1 in shape:
-        return tuple([st if n > 1 else 0 for n, st in zip(shape[:-1], stride)])
     return stride[:-1]
 
 
@@ -460,7 +460,7 @@ def _sections(style: str, sections: tuple):
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
     if not 1 <= len(sections) <= 3 or not all(0 <= n <= 2048 for n in sections):
         raise ValueError("one to three position axes, of 0 to 2048 pairs each")
-    return ROPE_STYLES[style], len(sections), (_c_int * 3)(*sections)
+    return ROPE_STYLES[style], len(sections), (_c_int * 3)(*map(int, sections))
 
 
 def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse: bool,
@@ -468,7 +468,7 @@ def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse
     if freqs.dim() != 1:
         raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
     n = freqs.shape[0]
-    code, axes, sec = _sections(style, (n,) if sections is None else tuple(map(int, sections)))
+    code, axes, sec = _sections(style, (n,) if sections is None else tuple(sections))
     return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, mscale,
                  1 if inverse else 0)
 
@@ -520,7 +520,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
     else:
         _arg(out, "out", x.dtype, shape, index, dense=False)
         ys = _rows(out, "out")
-        if (out.data_ptr() != x.data_ptr() or ys != xs) and not _apart(x, out):
+        if (out.data_ptr() != x.data_ptr() or any(
+                n > 1 and i != j for n, i, j in zip(shape, xs, ys))) and not _apart(x, out):
             raise ValueError("out may be x itself, but not share some of its elements")
     batched = pos.dim() == 3
     _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, _int64s(xs), p, B * N if batched else N,
@@ -580,8 +581,7 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
         oc = o + 12 * n_cap
         ol = oc + 4 * (R + 1)
         of = ol + 4 * R
-        slots, pos, req, cu, lens_out, count = buf.split_with_sizes(
-            (n_cap, n_cap, n_cap, R + 1, R, 1))
+        slots, pos, req, cu, lens_out, count = _pieces(buf, (n_cap, n_cap, n_cap, R + 1, R, 1))
         out = PagedPlan(cu, slots, pos, req, lens_out, count)
     else:
         oc, os_, op, oq, ol, of = [
@@ -609,7 +609,7 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
             return paged_release(done, lens, table, free_list, free_count, page, lens_out,
                                  free_count_out, status)
     if lens_out is None or free_count_out is None:
-        a, b = lens.new_empty(R + 1).split_with_sizes((R, 1))
+        a, b = _pieces(lens.new_empty(R + 1), (R, 1))
         lens_out = a if lens_out is None else lens_out
         free_count_out = b if free_count_out is None else free_count_out
     _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, page, num_pages,
