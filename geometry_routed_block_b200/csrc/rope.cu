@@ -26,6 +26,12 @@ namespace {
 
 constexpr int RT = 128;  // threads per CTA
 
+// The kernel after this one may be launched already; it waits for this grid's end before it
+// touches memory (the attention over the pages does).
+__device__ __forceinline__ void let_next_in() {
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
 __device__ __forceinline__ void turn(double freq, int pos, float mscale, float sign, float& c,
                                      float& s) {
     // h = t / pi as an unevaluated sum: 1/pi in two doubles, so that the
@@ -167,6 +173,7 @@ __device__ __forceinline__ long long token_slot(const RopeArgs& a, long long t, 
 template <typename TI, typename TO, bool SPLIT, int U>
 __global__ void __launch_bounds__(RT)
     rope_vec_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
+    let_next_in();
     const int l = threadIdx.x & ((1 << lanes_log2) - 1);
     const long long t =
         static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
@@ -236,6 +243,7 @@ template <int U>
 __global__ void __launch_bounds__(RT, 4)
     rope_half_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
     using T = __nv_bfloat16;
+    let_next_in();
     const int l = threadIdx.x & ((1 << lanes_log2) - 1);
     const long long t =
         static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
@@ -312,6 +320,7 @@ __global__ void __launch_bounds__(RT, 4)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(RT)
     rope_scalar_kernel(const __grid_constant__ RopeArgs a, int rows_per_y) {
+    let_next_in();
     const int l = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (RT / 32) + (threadIdx.x >> 5);
     if (t >= a.tokens) return;
