@@ -33,6 +33,12 @@ constexpr int BIG = 1024, SMALL = 256;  // threads per CTA
 constexpr int MAX_R = 8192;
 constexpr int CLUSTER = 8;              // CTAs of a cluster
 
+// as the rotary kernels: launches overlap, memory is touched in turn
+__device__ __forceinline__ void take_turn() {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // exclusive prefix over the CTA of two 64-bit values, and their totals; its barriers
 // order what the threads wrote to shared memory before
 template <int PT>
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const __grid_constant__ 
     const int per = (a.R + PT - 1) / PT;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
 
+    take_turn();
     if (threadIdx.x == 0) bad_any = 0;
     const int fc = *a.free_count;
     // bit 0: a length that cannot be, bit 1: a request beyond its table row
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const __grid_constant__ 
 // which is 0 throughout where the plan did not fit
 __global__ void __launch_bounds__(BIG) paged_plan_commit_kernel(const __grid_constant__ PlanArgs a) {
     __shared__ long long sh[2 * BIG / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    take_turn();
     const int fc = *a.free_count;
     int now[MAX_R / BIG];
     long long np = 0, none = 0, tp, tn;
@@ -244,6 +251,7 @@ __global__ void __launch_bounds__(PT) paged_release_kernel(const __grid_constant
     int* pg = sm;
     const int per = (a.R + PT - 1) / PT;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
+    take_turn();
     const Back k = count_back<PT>(a, r0, r1, sh, &bad_any);
     if (k.ok) {
         int p = k.first;
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(BIG)
     paged_release_commit_kernel(const __grid_constant__ PlanArgs a) {
     __shared__ long long sh[2 * BIG / 32];
     __shared__ int bad_any;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    take_turn();
     const int per = (a.R + BIG - 1) / BIG;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
     const Back k = count_back<BIG>(a, r0, r1, sh, &bad_any);
@@ -288,7 +296,7 @@ bool overlap(const int32_t* a, long long na, const int32_t* b, long long nb) {
 }
 
 int launch(void (*kern)(PlanArgs), const PlanArgs& a, int ctas, int threads, size_t smem,
-           bool cluster, bool after, cudaStream_t st) {
+           bool cluster, cudaStream_t st) {
     // static shared memory comes on top: raise the limit well before the default one
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -300,18 +308,14 @@ int launch(void (*kern)(PlanArgs), const PlanArgs& a, int ctas, int threads, siz
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    if (cluster) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = ctas;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.numAttrs = 1;
-    } else if (after) {
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.numAttrs = 1;
-    }
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? VELOX_OK : VELOX_ECUDA;
 }
 
@@ -325,14 +329,14 @@ int run(void (*small)(PlanArgs), void (*cluster)(PlanArgs), void (*big)(PlanArgs
                           overlap(a.lens_out, a.R, a.free_count, 1) ||
                           overlap(a.free_count_out, 1, a.add, a.R);
     a.later = 0;
-    if (items <= BIG && a.R <= BIG) return launch(small, a, 1, SMALL, smem, false, false, st);
+    if (items <= BIG && a.R <= BIG) return launch(small, a, 1, SMALL, smem, false, st);
     const int ctas = static_cast<int>(std::min<long long>((items + BIG - 1) / BIG, 148));
-    if (!in_place) return launch(big, a, ctas, BIG, smem, false, false, st);
+    if (!in_place) return launch(big, a, ctas, BIG, smem, false, st);
     if (items <= 2 * CLUSTER * BIG)
-        return launch(cluster, a, std::min(ctas, CLUSTER), BIG, smem, true, false, st);
+        return launch(cluster, a, std::min(ctas, CLUSTER), BIG, smem, true, st);
     a.later = 1;
-    const int rc = launch(big, a, ctas, BIG, smem, false, false, st);
-    return rc != VELOX_OK ? rc : launch(commit, a, 1, BIG, 0, false, true, st);
+    const int rc = launch(big, a, ctas, BIG, smem, false, st);
+    return rc != VELOX_OK ? rc : launch(commit, a, 1, BIG, 0, false, st);
 }
 
 }  // namespace

@@ -26,10 +26,12 @@ namespace {
 
 constexpr int RT = 128;  // threads per CTA
 
-// The kernel after this one may be launched already; it waits for this grid's end before it
-// touches memory (the attention over the pages does).
-__device__ __forceinline__ void let_next_in() {
+// The launch overlaps the end of the kernel before this one in the stream, and lets that of
+// the next one overlap this one's: nothing in memory is touched before the kernel before
+// has ended.
+__device__ __forceinline__ void take_turn() {
     asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ void turn(double freq, int pos, float mscale, float sign, float& c,
@@ -173,7 +175,7 @@ __device__ __forceinline__ long long token_slot(const RopeArgs& a, long long t, 
 template <typename TI, typename TO, bool SPLIT, int U>
 __global__ void __launch_bounds__(RT)
     rope_vec_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
-    let_next_in();
+    take_turn();
     const int l = threadIdx.x & ((1 << lanes_log2) - 1);
     const long long t =
         static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
@@ -243,7 +245,7 @@ template <int U>
 __global__ void __launch_bounds__(RT, 4)
     rope_half_kernel(const __grid_constant__ RopeArgs a, int lanes_log2, int rows_per_y) {
     using T = __nv_bfloat16;
-    let_next_in();
+    take_turn();
     const int l = threadIdx.x & ((1 << lanes_log2) - 1);
     const long long t =
         static_cast<long long>(blockIdx.x) * (RT >> lanes_log2) + (threadIdx.x >> lanes_log2);
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(RT, 4)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(RT)
     rope_scalar_kernel(const __grid_constant__ RopeArgs a, int rows_per_y) {
-    let_next_in();
+    take_turn();
     const int l = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * (RT / 32) + (threadIdx.x >> 5);
     if (t >= a.tokens) return;
@@ -378,15 +380,22 @@ int launch(const RopeArgs& a, bool vec, cudaStream_t st) {
     constexpr int U = BF ? 8 : 4;  // rows at once: 128 bytes of a thread
     // in the half layout an item's other half is a whole item, in the same warp
     const bool exchange = BF && a.rot > 0 && a.rot % 16 == 0 && a.d <= 256;
-    if (!vec)
-        rope_scalar_kernel<TI, TO><<<grid, RT, 0, st>>>(a, rows_per_y);
-    else if (!a.half_style)
-        rope_vec_kernel<TI, TO, false, U><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
-    else if (exchange)
-        rope_half_kernel<4><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
-    else
-        rope_vec_kernel<TI, TO, true, U><<<grid, RT, 0, st>>>(a, lanes_log2, rows_per_y);
-    return cudaGetLastError() == cudaSuccess ? VELOX_OK : VELOX_ECUDA;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(RT);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t rc =
+        !vec ? cudaLaunchKernelEx(&cfg, rope_scalar_kernel<TI, TO>, a, rows_per_y)
+        : !a.half_style
+            ? cudaLaunchKernelEx(&cfg, rope_vec_kernel<TI, TO, false, U>, a, lanes_log2, rows_per_y)
+        : exchange ? cudaLaunchKernelEx(&cfg, rope_half_kernel<4>, a, lanes_log2, rows_per_y)
+                   : cudaLaunchKernelEx(&cfg, rope_vec_kernel<TI, TO, true, U>, a, lanes_log2, rows_per_y);
+    return rc == cudaSuccess ? VELOX_OK : VELOX_ECUDA;
 }
 
 }  // namespace
