@@ -226,6 +226,7 @@ __device__ __forceinline__ void next_row(const PagedAttnArgs& a, Row& p) {
         ++p.r;
         p.n = p.r < a.R ? clamp_len(a.lens[p.r], a.max_pages * a.page) : UNIT;
     } while (p.n == 0);
+    p.r = min(p.r, a.R - 1);  // reached only if the lengths change meanwhile: stay within the table
     p.units = units_of(p.n);
 }
 

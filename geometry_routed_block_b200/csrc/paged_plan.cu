@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const __grid_constant__ 
     long long nt = 0, np = 0;
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r], m = a.add[r];
+        old[r] = n, tok[r] = m;  // read once: what follows agrees with what was counted
         if (n < 0 || n > cap || m < 0) {
             bad |= 1;
             continue;
@@ -133,10 +134,9 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const __grid_constant__ 
         new_pages = static_cast<int>(tp);
         int t = static_cast<int>(t0), p = static_cast<int>(p0);
         for (int r = r0; r < r1; ++r) {
-            const int n = a.lens[r], m = a.add[r];
+            const int n = old[r], m = tok[r];
             tok[r] = t;
             pg[r] = p;
-            old[r] = n;
             t += m;
             p += pages_of(n + m, a.page_shift) - pages_of(n, a.page_shift);
         }
@@ -213,14 +213,15 @@ __global__ void __launch_bounds__(BIG) paged_plan_commit_kernel(const __grid_con
 }
 
 // Whether the pages of the requests that end (a.add != 0) can go back, how many they
-// are, and where this thread's requests (r0 .. r1 - 1) begin among them.
+// are (each request's own in count[], if given), and where this thread's requests (r0 ..
+// r1 - 1) begin among them.
 struct Back {
     int fc, pages, first;
     bool ok, bad;
 };
 template <int PT>
 __device__ __forceinline__ Back count_back(const PlanArgs& a, int r0, int r1, long long* sh,
-                                           int* bad_any) {
+                                           int* bad_any, int* count) {
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
     if (threadIdx.x == 0) *bad_any = 0;
     Back k;
@@ -229,8 +230,10 @@ __device__ __forceinline__ Back count_back(const PlanArgs& a, int r0, int r1, lo
     long long np = 0, none = 0, tp, tn;
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r];
+        const int c = n >= 0 && n <= cap && a.add[r] != 0 ? pages_of(n, a.page_shift) : 0;
         if (n < 0 || n > cap) bad = 1;
-        else if (a.add[r] != 0) np += pages_of(n, a.page_shift);
+        if (count) count[r] = c;
+        np += c;
     }
     __syncthreads();
     if (bad) *bad_any = 1;
@@ -252,12 +255,13 @@ __global__ void __launch_bounds__(PT) paged_release_kernel(const __grid_constant
     const int per = (a.R + PT - 1) / PT;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
     take_turn();
-    const Back k = count_back<PT>(a, r0, r1, sh, &bad_any);
+    const Back k = count_back<PT>(a, r0, r1, sh, &bad_any, pg);
     if (k.ok) {
         int p = k.first;
         for (int r = r0; r < r1; ++r) {
+            const int c = pg[r];
             pg[r] = p;
-            if (a.add[r] != 0) p += pages_of(a.lens[r], a.page_shift);
+            p += c;
         }
     }
     if (ONE_CLUSTER) cluster_sync();  // lengths and count read by every CTA
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(BIG)
     take_turn();
     const int per = (a.R + BIG - 1) / BIG;
     const int r0 = min(a.R, static_cast<int>(threadIdx.x) * per), r1 = min(a.R, r0 + per);
-    const Back k = count_back<BIG>(a, r0, r1, sh, &bad_any);
+    const Back k = count_back<BIG>(a, r0, r1, sh, &bad_any, nullptr);
     for (int r = r0; r < r1; ++r) a.lens_out[r] = (k.ok && a.add[r] != 0) ? 0 : a.lens[r];
     if (threadIdx.x == 0) *a.free_count_out = k.fc + k.pages;
 }
