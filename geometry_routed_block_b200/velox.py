@@ -523,6 +523,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
         if (out.data_ptr() != x.data_ptr() or any(
                 n > 1 and i != j for n, i, j in zip(shape, xs, ys))) and not _apart(x, out):
             raise ValueError("out may be x itself, but not share some of its elements")
+    if 0 in shape:
+        return out  # nothing to turn
     batched = pos.dim() == 3
     _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, _int64s(xs), p, B * N if batched else N,
                           N if batched else 0, ctypes.byref(spec), out.data_ptr(), _int64s(ys),
@@ -669,6 +671,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     elif q is not None:
         out = q.new_empty((N, H, d)) if dt == VELOX_BF16 else q.new_empty((N, H, d), dtype=_BF16)
         po = out.data_ptr()
+    if N == 0:
+        return out  # no tokens
     _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
                                   spec, po, kp, vp, page, num_pages, ps, _raw_stream(index)),
            "velox_paged_append")
@@ -713,7 +717,9 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     if there is not None:
         with there:
             return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status)
-    if ws is not None:
+    if R == 0:
+        pw, nw = None, 0
+    elif ws is not None:
         pw, nw = _arg(ws, "ws", torch.uint8, None, index), ws.numel()
     elif _needs_no_workspace(R * Hkv * ((H // max(Hkv, 1) + 15) // 16), width * page):
         pw, nw = None, 0
@@ -734,6 +740,8 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         pe = lse.data_ptr()
     else:
         pe = _arg(lse, "lse", _F32, (R, H), index)
+    if R == 0:
+        return out, lse  # no requests
     _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
                                 1.0 / math.sqrt(d) if scale is None else scale, po, pe, pw,
                                 nw, ps, _raw_stream(index)), "velox_paged_attn")

@@ -794,6 +794,23 @@ def test_calls_on_a_given_stream(vx):
     assert torch.equal(got, want)
 
 
+def test_nothing_to_do(vx):
+    """No tokens, no requests: empty results, nothing written."""
+    f = torch.tensor(freqs_for((32,)), device="cuda")
+    e = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    assert vx.rope(e(2, 3, 0, 64), e(1, 0, t=I32), f).shape == (2, 3, 0, 64)
+    kp = torch.ones(2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    vp = kp.clone()
+    q = vx.paged_append(e(0, 2, 64), e(0, 2, 64), e(0, t=I32), kp, vp, q=e(0, 4, 64), pos=e(0, t=I32), freqs=f)
+    assert q.shape == (0, 4, 64) and q.dtype == torch.bfloat16
+    assert vx.paged_append(e(0, 2, 64), e(0, 2, 64), e(0, t=I32), kp, vp) is None
+    o, lse = vx.paged_attn(e(0, 4, 64), kp, vp, e(0, 5, t=I32), e(0, t=I32))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    assert (kp == 1).all() and (vp == 1).all()
+    with pytest.raises(vx.VeloxError):      # a cache without requests is not planned
+        vx.paged_plan(e(0, t=I32), e(0, t=I32), e(0, 5, t=I32), i32([0]), i32([1]), 16, 4)
+
+
 def test_cache_reports_and_recovers(vx):
     from geometry_routed_block_b200.paged import PagedCache
     c = PagedCache(1, 2, 1, 64, 16, 4, 4)
