@@ -11,8 +11,8 @@
 // rate, so the products run on warp-level matrix instructions, whose 16 rows
 // suit the few query heads (a 128-row tile would be padding), and everything
 // else serves the stream of loads:
-//   - The history is cut in units of 16 tokens (K and V of one key head: 8 KB at
-//     d = 128). The units of all (request, key head, tile of query heads) rows are
+//   - The history is cut in units of 8 KB (K and V of one key head: 16 tokens at d = 128, 32
+//     at d = 64). The units of all (request, key head, tile of query heads) rows are
 //     numbered in order, with ROW_COST empty units behind each row for what a
 //     row costs beyond its units, and every warp takes an equal, contiguous share,
 //     whatever the lengths are; no length is read by the host. Rows that lie
@@ -45,7 +45,7 @@ namespace velox {
 
 namespace {
 
-constexpr int UNIT = 16;       // tokens per unit: the smallest page
+constexpr int BOX = 16;        // tokens that one load fetches: the smallest page
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most
@@ -61,21 +61,23 @@ constexpr int ROW_COST = 2;    // empty units that a row counts for
 // units per warp at least: fewer would cost more joining than they save
 constexpr int MIN_SHARE = 2;
 
-// Where no row can be longer (by the width of the table) than so many units for each of the
+// Where no row can be longer (by the width of the table) than so many tokens for each of the
 // n = 1, 2, 4 or 8 CTAs that every row can have at once, rows are not dealt out by length:
 // a CTA or a cluster takes a row, in one launch and without a workspace. 32 / 8 heads, one
 // request: 20 tokens 4.8 us, 257 tokens 6.5 us (one CTA a row 8.4, dealt out 9.1), 480 tokens 6.7
 // us (10.6, 9.2); 1024 tokens with one CTA a row 16.4 us, dealt out 9.4.
-constexpr int WHOLE_UNITS = 32, WHOLE_CTAS = 256;
+constexpr int WHOLE_TOKENS = 512, WHOLE_CTAS = 256;
 
 template <int D, int MT>
 struct Cfg {
     static constexpr int HEADS = 8 * MT;           // query heads per tile
-    static constexpr int HALF = UNIT * 128;        // 16 tokens x 64 columns
+    static constexpr int SUB = 128 / D;            // boxes of 16 tokens in a unit
+    static constexpr int UNIT = SUB * BOX;         // tokens of a unit: 8 KB of K and V
+    static constexpr int HALF = BOX * 128;         // a box: 16 tokens x 64 columns
     static constexpr int TILE = UNIT * D * 2;      // K or V of a unit
     static constexpr int STAGE = 2 * TILE;
     // units that a warp's ring has room for with two CTAs per SM (the launch may use fewer)
-    static constexpr int ST = (D == 128 ? 3 : 6) - (MT == 2 ? (D == 128 ? 1 : 2) : 0);
+    static constexpr int ST = MT == 2 ? 2 : 3;
     static constexpr int OFF_O = NW * ST * STAGE;  // float [NW][HEADS][D]: a warp's first row
     static constexpr int OFF_M = OFF_O + NW * HEADS * D * 4;   // float [2 NW][HEADS]
     static constexpr int OFF_L = OFF_M + 2 * NW * HEADS * 4;   // float [2 NW][HEADS]
@@ -89,7 +91,11 @@ struct Cfg {
 };
 
 __device__ __forceinline__ int clamp_len(int n, int cap) { return min(max(n, 0), cap); }
-__device__ __forceinline__ int units_of(int n) { return (n + UNIT - 1) / UNIT; }
+template <int D>
+__device__ __forceinline__ int units_of(int n) {
+    constexpr int UNIT = Cfg<D, 1>::UNIT;
+    return n / UNIT + (n % UNIT != 0);
+}
 
 // A row: one key head (and tile of its query heads) of one request. Its real units
 // are base .. base + units - 1 in the numbering of all, ROW_COST empty ones follow.
@@ -130,7 +136,7 @@ __device__ __forceinline__ int weight(int units) { return units > 0 ? units + RO
 // gets the i-th's row (nothing where there is no such share, or an empty one at the
 // end). sh: 6 long longs per share, and one per warp at least. The caller lets the
 // CTA meet before it reads sh.
-template <int THREADS>
+template <int D, int THREADS>
 __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int count, int step,
                                        long long* sh, bool report) {
     const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
@@ -147,12 +153,12 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
     for (int i = 0; i < KEPT; ++i) {
         bad |= kept[i] < 0 || kept[i] > cap;
         kept[i] = clamp_len(kept[i], cap);
-        mine += weight(units_of(kept[i]));
+        mine += weight(units_of<D>(kept[i]));
     }
     for (int r = r0 + KEPT; r < r1; ++r) {
         const int n = a.lens[r];
         bad |= n < 0 || n > cap;
-        mine += weight(units_of(clamp_len(n, cap)));
+        mine += weight(units_of<D>(clamp_len(n, cap)));
     }
     if (report && bad && a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
     long long x = mine;
@@ -187,17 +193,17 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
 #pragma unroll
         for (int i = 0; i < KEPT; ++i) {
             if (r >= 0) continue;
-            const long long next = at + static_cast<long long>(weight(units_of(kept[i]))) * rows;
+            const long long next = at + static_cast<long long>(weight(units_of<D>(kept[i]))) * rows;
             if (s < next) r = r0 + i, n = kept[i];
             else at = next;
         }
         for (int i = r0 + KEPT; r < 0 && i < r1; ++i) {
             n = clamp_len(a.lens[i], cap);
-            const long long next = at + static_cast<long long>(weight(units_of(n))) * rows;
+            const long long next = at + static_cast<long long>(weight(units_of<D>(n))) * rows;
             if (s < next) r = i;
             else at = next;
         }
-        un = units_of(n);
+        un = units_of<D>(n);
         const int row = static_cast<int>(quotient(s - at, weight(un)));
         sh[6 * w] = at + static_cast<long long>(row) * weight(un);
         sh[6 * w + 1] = r;
@@ -207,27 +213,29 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
     return k;
 }
 
+template <int D>
 __device__ __forceinline__ Row located(const long long* sh) {
     Row p;
     p.base = sh[0];
     p.r = static_cast<int>(sh[1]);
     p.row = static_cast<int>(sh[2]);
     p.n = static_cast<int>(sh[3]);
-    p.units = units_of(p.n);
+    p.units = units_of<D>(p.n);
     return p;
 }
 
 // the next row that has units (the caller knows that there is one)
+template <int D>
 __device__ __forceinline__ void next_row(const PagedAttnArgs& a, Row& p) {
     p.base += weight(p.units);
     if (++p.row < a.Hkv * a.head_tiles) return;
     p.row = 0;
     do {
         ++p.r;
-        p.n = p.r < a.R ? clamp_len(a.lens[p.r], a.max_pages * a.page) : UNIT;
+        p.n = p.r < a.R ? clamp_len(a.lens[p.r], a.max_pages * a.page) : 1;
     } while (p.n == 0);
     p.r = min(p.r, a.R - 1);  // reached only if the lengths change meanwhile: stay within the table
-    p.units = units_of(p.n);
+    p.units = units_of<D>(p.n);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(NT, 2)
         p.row = row - p.r * rows;
         const int n = a.lens[p.r];
         p.n = clamp_len(n, cap);
-        p.units = units_of(p.n);
+        p.units = units_of<D>(p.n);
         if (p.row == 0 && threadIdx.x == 0 && n != p.n && a.status)
             atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
         const int pieces = a.whole_rows * NW;
@@ -451,63 +459,78 @@ __global__ void __launch_bounds__(NT, 2)
         if (p.n == 0 && p.row == 0 && piece < NW) empty_rows<D>(a, p.r, a.R, cap);
         if (p.n == 0) return;
     } else {
-        const Work work = locate<NT>(a, cta * NW, NW, 1, sh, cta == 0);
+        const Work work = locate<D, NT>(a, cta * NW, NW, 1, sh, cta == 0);
         __syncthreads();  // rows found, barriers initialised
         if (cta >= work.grid || work.total == 0) {
             empty_rows<D>(a, cta, gridDim.x, cap);
             return;
         }
         g0 = work.start(cta * NW + warp), g1 = work.start(cta * NW + warp + 1);
-        p = located(sh + 6 * warp);
+        p = located<D>(sh + 6 * warp);
     }
 
     // ---- loads, ahead of the products and across rows. f: the row of the next unit to
     // fetch, fu .. fend - 1 what is left of it in the share. Lane i keeps the page id of
-    // the row's unit ids_at + i
+    // the row's box ids_at + i
+    constexpr int SUB = C::SUB, UNIT = C::UNIT;
     Row f = p;
     int fu = 0, fend = 0, ids_at = 0, ids = 0;
     bool more = g0 < g1;  // units are left to fetch
     const auto look_up = [&]() {
-        ids_at = fu;
-        if (fu + lane < fend)
-            ids = a.table[static_cast<long long>(f.r) * a.max_pages +
-                          (((fu + lane) * UNIT) >> a.page_shift)];
+        ids_at = fu * SUB;
+        const int box = ids_at + lane;
+        if (box < fend * SUB && box * BOX < f.n)
+            ids = a.table[static_cast<long long>(f.r) * a.max_pages + ((box * BOX) >> a.page_shift)];
     };
     if (more) {
         fu = static_cast<int>(g0 - f.base);
         fend = static_cast<int>(min(g1 - f.base, static_cast<long long>(f.units)));
     }
-    const auto settle = [&]() {  // fu to a unit that is there, its page id to a lane
+    const auto settle = [&]() {  // fu to a unit that is there, its page ids to lanes
         while (more && fu >= fend) {
             if (f.base + weight(f.units) >= g1) {
                 more = false;
             } else {
-                next_row(a, f);
+                next_row<D>(a, f);
                 fu = 0;
                 fend = static_cast<int>(min(g1 - f.base, static_cast<long long>(f.units)));
                 ids_at = -32;
             }
         }
-        if (more && fu - ids_at >= 32) look_up();
+        if (more && (fu + 1) * SUB - ids_at > 32) look_up();
     };
-    ids_at = fu - 32;
+    ids_at = fu * SUB - 32;
     settle();
     const auto fetch = [&](int slot) {
-        const int found = __shfl_sync(~0u, ids, fu - ids_at);
+        int found[SUB];
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            found[i] = __shfl_sync(~0u, ids, fu * SUB + i - ids_at);
+            // a last unit may end in its first box: the second then is any page that is there
+            if (i > 0 && (fu * SUB + i) * BOX >= f.n) found[i] = found[0];
+        }
         if (lane == 0) {
-            int id = found;
-            if (id < 0 || id >= a.num_pages) {
-                if (a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
-                id = 0;
-            }
-            const int y = (id * a.Hkv + f.row / a.head_tiles) * a.page + ((fu * UNIT) & (a.page - 1));
             const uint32_t bar = bars + 8 * slot, dst = ring + slot * C::STAGE;
             mbar_arrive_expect_tx(bar, C::STAGE);
+            int y[SUB];
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) tma_load_2d(dst + h * C::HALF, &tmK, bar, 64 * h, y);
+            for (int i = 0; i < SUB; ++i) {
+                int id = found[i];
+                if (id < 0 || id >= a.num_pages) {
+                    if (a.status) atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
+                    id = 0;
+                }
+                y[i] = (id * a.Hkv + f.row / a.head_tiles) * a.page +
+                       (((fu * SUB + i) * BOX) & (a.page - 1));
+            }
+            // D = 128: the two column halves of a box; D = 64: two boxes
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-                tma_load_2d(dst + C::TILE + h * C::HALF, &tmV, bar, 64 * h, y);
+            for (int i = 0; i < 2; ++i)
+                tma_load_2d(dst + i * C::HALF, &tmK, bar, SUB == 1 ? 64 * i : 0, y[SUB == 1 ? 0 : i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                tma_load_2d(dst + C::TILE + i * C::HALF, &tmV, bar, SUB == 1 ? 64 * i : 0,
+                            y[SUB == 1 ? 0 : i]);
         }
         ++fu;
         settle();
@@ -572,33 +595,40 @@ __global__ void __launch_bounds__(NT, 2)
                     fence_proxy_async_smem();  // before the next fetch into this slot
                     __syncwarp();
                 }
-                // S: two key groups of 8, each in two chains over d
-                float s[2][2][4];
+                // S: two key groups of 8 per box, at d = 128 each in two chains over d
+                constexpr int KG = 2 * SUB, CH = SUB == 1 ? 2 : 1;
+                float s[CH][KG][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < CH; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
+                    for (int j = 0; j < KG; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    uint32_t b[4];  // keys 0-7: d lo, d hi; keys 8-15: d lo, d hi
-                    ldsm4(kt + tile_at<D, MT>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)),
-                          b);
                     const uint32_t a1 = MT == 2 ? q[MT - 1][k][0] : 0u;
                     const uint32_t a3 = MT == 2 ? q[MT - 1][k][1] : 0u;
-                    mma16816(s[k & 1][0], q[0][k][0], a1, q[0][k][1], a3, b[0], b[1]);
-                    mma16816(s[k & 1][1], q[0][k][0], a1, q[0][k][1], a3, b[2], b[3]);
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) {
+                        uint32_t b[4];  // keys 0-7 of the box: d lo, d hi; keys 8-15: d lo, d hi
+                        ldsm4(kt + tile_at<D, MT>(BOX * x + (lane & 7) + ((lane >> 4) << 3),
+                                                  2 * k + ((lane >> 3) & 1)),
+                              b);
+                        mma16816(s[k % CH][2 * x], q[0][k][0], a1, q[0][k][1], a3, b[0], b[1]);
+                        mma16816(s[k % CH][2 * x + 1], q[0][k][0], a1, q[0][k][1], a3, b[2], b[3]);
+                    }
                 }
-                uint32_t hi[MT][2], lo[MT][2];
+                uint32_t hi[MT][KG], lo[MT][KG];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    float x[4];  // keys 2t, 2t+1, 8+2t, 8+2t+1 of head 8 i + g
+                    float x[2 * KG];  // keys 8 j + 2t, 8 j + 2t + 1 of head 8 i + g
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[j] = (s[0][j >> 1][2 * i + (j & 1)] + s[1][j >> 1][2 * i + (j & 1)]) *
-                               a.scale_log2;
+                    for (int j = 0; j < 2 * KG; ++j) {
+                        x[j] = s[0][j >> 1][2 * i + (j & 1)];
+                        if (CH == 2) x[j] += s[CH - 1][j >> 1][2 * i + (j & 1)];
+                        x[j] *= a.scale_log2;
                         if (8 * (j >> 1) + 2 * t + (j & 1) >= valid) x[j] = -INFINITY;
+                        top = fmaxf(top, x[j]);
                     }
-                    float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     const float m_new = fmaxf(m[i], top);
@@ -613,28 +643,30 @@ __global__ void __launch_bounds__(NT, 2)
                         }
                         m[i] = m_new;
                     }
-                    const float ref = m[i] == -INFINITY ? 0.0f : m[i];
-                    float pr[4];
+                    const float ref = finite_ref(m[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) pr[j] = ex2_approx(x[j] - ref);
-                    l[i] += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        hi[i][j] = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
-                        lo[i][j] = pack_bf16x2(pr[2 * j] - bf16_lo(hi[i][j]),
-                                               pr[2 * j + 1] - bf16_hi(hi[i][j]));
+                    for (int j = 0; j < KG; ++j) {
+                        const float p0 = ex2_approx(x[2 * j] - ref), p1 = ex2_approx(x[2 * j + 1] - ref);
+                        l[i] += p0 + p1;
+                        hi[i][j] = pack_bf16x2(p0, p1);
+                        lo[i][j] = pack_bf16x2(p0 - bf16_lo(hi[i][j]), p1 - bf16_hi(hi[i][j]));
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    uint32_t b[4];  // d 16 j .. +7: keys lo, keys hi; the next 8: keys lo, keys hi
-                    ldsm4_t(vt + tile_at<D, MT>((lane & 7) + (((lane >> 3) & 1) << 3),
-                                                2 * j + (lane >> 4)),
-                            b);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        mma16816(o[i][2 * j], hi[i][0], lo[i][0], hi[i][1], lo[i][1], b[0], b[1]);
-                        mma16816(o[i][2 * j + 1], hi[i][0], lo[i][0], hi[i][1], lo[i][1], b[2], b[3]);
+                    for (int x = 0; x < SUB; ++x) {
+                        uint32_t b[4];  // d 16 j .. +7: keys lo, keys hi; the next 8: keys lo, keys hi
+                        ldsm4_t(vt + tile_at<D, MT>(BOX * x + (lane & 7) + (((lane >> 3) & 1) << 3),
+                                                    2 * j + (lane >> 4)),
+                                b);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            const uint32_t h0 = hi[i][2 * x], h1 = hi[i][2 * x + 1];
+                            const uint32_t l0 = lo[i][2 * x], l1 = lo[i][2 * x + 1];
+                            mma16816(o[i][2 * j], h0, l0, h1, l1, b[0], b[1]);
+                            mma16816(o[i][2 * j + 1], h0, l0, h1, l1, b[2], b[3]);
+                        }
                     }
                 }
                 __syncwarp();  // every lane has read the slot
@@ -696,7 +728,7 @@ __global__ void __launch_bounds__(NT, 2)
             }
         }
         if (p.base + weight(p.units) >= g1) break;
-        next_row(a, p);
+        next_row<D>(a, p);
     }
     // a wait that ran out: what is still in flight lands before the CTA leaves
     if (!ok) {
@@ -766,7 +798,7 @@ __global__ void __launch_bounds__(JT)
     __shared__ float red_m[JW], red_l[JW];
     __shared__ float4 red_o[JW][LANES];
     const int c = blockIdx.x;
-    const Work work = locate<JT>(a, c * NW, 2, NW, sh, false);
+    const Work work = locate<D, JT>(a, c * NW, 2, NW, sh, false);
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the row that share c goes on with, and the one it begins and leaves. All of this
@@ -778,7 +810,7 @@ __global__ void __launch_bounds__(JT)
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             if (side == 1 && c + 1 >= work.grid) break;
-            const Row p = located(sh + 6 * side);
+            const Row p = located<D>(sh + 6 * side);
             const long long end = p.base + p.units;
             if (side == 0 ? (s0 <= p.base || s0 >= end)
                           : (p.base < s0 || s1 <= p.base || s1 >= end))
@@ -911,7 +943,7 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     static_assert(C::HALF % 1024 == 0, "swizzle atoms");
     CUtensorMap tk, tv;
     const uint64_t pool = static_cast<uint64_t>(a.num_pages) * a.Hkv * a.page;
-    if (!make_tmap(&tk, k_pages, pool, D, UNIT) || !make_tmap(&tv, v_pages, pool, D, UNIT))
+    if (!make_tmap(&tk, k_pages, pool, D, BOX) || !make_tmap(&tv, v_pages, pool, D, BOX))
         return VELOX_ECUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -919,7 +951,7 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
         return VELOX_ECUDA;
     const int resident = std::min(7 * sms / 4, MAX_GRID);
     const long long rows = static_cast<long long>(a.R) * a.Hkv * a.head_tiles;
-    const long long units = static_cast<long long>(a.max_pages) * a.page / UNIT;
+    const long long units = static_cast<long long>(a.max_pages) * a.page / C::UNIT + 1;
     a.whole_rows = ctas_per_row(a, rows);
     // no more CTAs than the longest histories could keep busy
     a.grid = static_cast<int>(
@@ -966,11 +998,11 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
 
 int paged_attn_whole(int R, int H, int Hkv, int page, int max_pages) {
     const long long rows = static_cast<long long>(R) * Hkv * ((H / Hkv + 15) / 16);
-    const long long units = static_cast<long long>(max_pages) * page / UNIT;
+    const long long tokens = static_cast<long long>(max_pages) * page;
     int n = 8;
     while (n > 0 && rows * n > WHOLE_CTAS) n /= 2;
-    if (units > static_cast<long long>(WHOLE_UNITS) * n) return 0;
-    while (n > 1 && units < NW / 2 * n) n /= 2;  // a unit for every other warp
+    if (tokens > static_cast<long long>(WHOLE_TOKENS) * n) return 0;
+    while (n > 1 && tokens < NW / 2 * BOX * n) n /= 2;  // a box for every other warp
     return n;
 }
 
