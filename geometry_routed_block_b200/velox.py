@@ -469,7 +469,7 @@ def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse
         raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
     n = freqs.shape[0]
     code, axes, sec = _sections(style, (n,) if sections is None else tuple(sections))
-    return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, mscale,
+    return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, float(mscale),
                  1 if inverse else 0)
 
 
@@ -569,6 +569,7 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pa = _arg(add, "add", _I32, (R,), index)
     ps = None if status is None else _arg(status, "status", _I32, None, index)
+    page, n_cap = int(page), int(n_cap)
     if not 0 <= n_cap < 2 ** 31:
         raise ValueError("n_cap must be in [0, 2^31)")
     there = _elsewhere(lens, stream)
@@ -614,7 +615,7 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
         a, b = _pieces(lens.new_empty(R + 1), (R, 1))
         lens_out = a if lens_out is None else lens_out
         free_count_out = b if free_count_out is None else free_count_out
-    _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, page, num_pages,
+    _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, int(page), num_pages,
                                    _arg(lens_out, "lens_out", _I32, (R,), index),
                                    _arg(free_count_out, "free_count_out", _I32, (1,), index), ps,
                                    _raw_stream(index)), "velox_paged_release")
@@ -743,6 +744,6 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     if R == 0:
         return out, lse  # no requests
     _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
-                                1.0 / math.sqrt(d) if scale is None else scale, po, pe, pw,
+                                1.0 / math.sqrt(d) if scale is None else float(scale), po, pe, pw,
                                 nw, ps, _raw_stream(index)), "velox_paged_attn")
     return out, lse

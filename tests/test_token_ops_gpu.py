@@ -228,7 +228,8 @@ def test_plan_in_place_equals_out_of_place_and_allows_no_tokens(vx):
     lt, ct, tab = i32(lens), i32([len(free)]), i32(table)
     e = lambda n: torch.empty(n, dtype=I32, device="cuda")  # noqa: E731
     out = vx.PagedPlan(e(5), e(64), e(64), e(64), lt, ct)
-    vx.paged_plan(i32(add), lt, tab, i32(free + [0] * (num - len(free))), ct, page, 64, out=out)
+    vx.paged_plan(i32(add), lt, tab, i32(free + [0] * (num - len(free))), ct, np.int64(page), np.int64(64),
+                  out=out)
     for x, y in zip(a, out):
         assert torch.equal(x, y)
     assert torch.equal(tab, tab_a)
