@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(NT, 2)
     constexpr int SUB = C::SUB, UNIT = C::UNIT;
     Row f = p;
     int fu = 0, fend = 0, ids_at = 0, ids = 0;
-    bool more = g0 < g1;  // units are left to fetch
+    // units are left to fetch (test hook: a warp that fetches nothing waits in vain)
+    bool more = g0 < g1 && !(a.skip_warps >> warp & 1);
     const auto look_up = [&]() {
         ids_at = fu * SUB;
         const int box = ids_at + lane;
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(NT, 2)
         if (lane == 0 && a.status) atomicOr(a.status, VELOX_STATUS_TIMEOUT);
         volatile int never = 0;
         for (; ahead > 0; --ahead) {
-            if (!mbar_wait(bars + 8 * slot, parity, &never, a.wait_ns)) break;
+            if (!mbar_wait(bars + 8 * slot, parity, &never, WAIT_LIMIT_NS)) break;
             if (++slot == a.stages) slot = 0, parity ^= 1;
         }
     }
@@ -772,7 +773,9 @@ __global__ void __launch_bounds__(NT, 2)
             if (h >= heads) break;
             if (begins && ends) {
                 store_head<D>(a, q_row + h, col, j.acc[k], j.top[k], j.sum[k]);
-            } else {
+            } else if (!a.whole_rows) {
+                // (a CTA's own row lacks entries only after a wait that ran out, and then
+                // there may be no workspace)
                 *reinterpret_cast<float4*>(part + h * D + col) = j.acc[k];
                 if (col == 0) {
                     part[C::HEADS * D + h] = j.top[k];

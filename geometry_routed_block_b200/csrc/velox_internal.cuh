@@ -133,7 +133,8 @@ struct PagedAttnArgs {
     float* lse;
     float* part;     // workspace: partial results
     int32_t* status;
-    unsigned long long wait_ns;
+    unsigned long long wait_ns;  // limit of every bounded wait
+    int skip_warps;              // test hook: bit w: warp w of every CTA fetches nothing
 };
 // CTAs per row where histories are so short that rows are not dealt out by length, and no
 // workspace is needed; else 0

@@ -87,6 +87,8 @@ SIGNATURES = {
     "velox_paged_attn_workspace_size": (_c_size, [_c_int] * 4),
     "velox_paged_attn": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size, _vp,
                                                              _vp]),
+    "velox_paged_attn_test": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size,
+                                                                  _vp, _c_double, _c_int, _vp]),
 }
 
 
@@ -746,4 +748,23 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
                                 1.0 / math.sqrt(d) if scale is None else float(scale), po, pe, pw,
                                 nw, ps, _raw_stream(index)), "velox_paged_attn")
+    return out, lse
+
+
+def paged_attn_test(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    table: torch.Tensor, lens: torch.Tensor, status: torch.Tensor,
+                    wait_limit_s: float, skip_warps: int, ws: torch.Tensor | None = None):
+    """paged_attn through the test entry point (bounded-wait limit, and the warps that fetch
+    nothing); returns (O, lse), undefined where the waits ran out."""
+    R, H, d = q.shape
+    num_pages, Hkv, page, _ = k_pages.shape
+    _expect(q, _BF16, "q")
+    for t, n in ((table, "table"), (lens, "lens"), (status, "status")):
+        _expect(t, _I32, n)
+    out, lse = torch.empty_like(q), q.new_empty((R, H), dtype=_F32)
+    _check(lib.velox_paged_attn_test(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), R, H, Hkv, d, page, num_pages,
+        table.shape[1], 1.0 / math.sqrt(d), _ptr(out), _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel(), _ptr(status), float(wait_limit_s), int(skip_warps),
+        _stream()), "velox_paged_attn_test")
     return out, lse

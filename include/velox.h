@@ -498,7 +498,8 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  * joined in a fixed order: results do not change from call to call.
  * Page ids outside [0, num_pages) are replaced by page 0 and lens outside
  * [0, max_pages * page] by the nearer bound; both set VELOX_STATUS_BAD_INDEX.
- * An expired internal wait sets VELOX_STATUS_TIMEOUT (outputs then undefined).
+ * An expired internal wait sets VELOX_STATUS_TIMEOUT (outputs then undefined; nothing else
+ * is written).
  * Errors: VELOX_EINVAL for R < 1 or R > 65535, H < 1, H not a multiple of Hkv,
  * scale not positive and finite, max_pages or num_pages < 1, max_pages * page or
  * num_pages * Hkv * page >= 2^31, R * H >= 2^31, ws_bytes too small, NULL or
@@ -510,6 +511,19 @@ VELOX_API int velox_paged_attn(const void* q, const void* k_pages, const void* v
                                int d, int page, int num_pages, int max_pages, float scale,
                                void* o, float* lse, void* ws, size_t ws_bytes, int32_t* status,
                                void* stream);
+
+/*
+ * Test entry point: velox_paged_attn with a chosen limit for its bounded waits (1e-3 to
+ * 10 s; the copies in flight are waited for with the default limit) and, bit w of
+ * skip_warps (0 to 15), without the loads of warp w of every CTA, whose wait then runs
+ * out. Not for product use.
+ */
+VELOX_API int velox_paged_attn_test(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* table, const int32_t* lens, int R, int H,
+                                    int Hkv, int d, int page, int num_pages, int max_pages,
+                                    float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                                    int32_t* status, double wait_limit_s, int skip_warps,
+                                    void* stream);
 
 /*
  * Measurement helper, not a step of the method: blocks x threads threads each
