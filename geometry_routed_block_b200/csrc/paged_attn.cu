@@ -124,6 +124,7 @@ __device__ __forceinline__ long long quotient(long long x, long long d) {
 }
 
 __device__ __forceinline__ int Work::cta_of(long long u) const {
+    u = min(u, total - 1);
     const long long first = more * (each + 1);
     const long long w = u < first ? quotient(u, each + 1) : more + quotient(u - first, each);
     return static_cast<int>(w) / NW;
@@ -135,7 +136,8 @@ __device__ __forceinline__ int weight(int units) { return units > 0 ? units + RO
 // `count` warp shares begin, those numbered first, first + step, ...: sh[6 i] onwards
 // gets the i-th's row (nothing where there is no such share, or an empty one at the
 // end). sh: 6 long longs per share, and one per warp at least. The caller lets the
-// CTA meet before it reads sh.
+// CTA meet before it reads sh. Lengths beyond KEPT a thread are looked at twice: should one
+// change meanwhile, what is found is meaningless, but lies within the arguments.
 template <int D, int THREADS>
 __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int count, int step,
                                        long long* sh, bool report) {
@@ -203,9 +205,12 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
             if (s < next) r = i;
             else at = next;
         }
+        if (r < 0) r = r1 - 1;
         un = units_of<D>(n);
-        const int row = static_cast<int>(quotient(s - at, weight(un)));
-        sh[6 * w] = at + static_cast<long long>(row) * weight(un);
+        const int each_row = weight(un);
+        const int row = static_cast<int>(
+            min(quotient(s - at, max(each_row, 1)), static_cast<long long>(rows - 1)));
+        sh[6 * w] = max(at + static_cast<long long>(row) * each_row, s - each_row);
         sh[6 * w + 1] = r;
         sh[6 * w + 2] = row;
         sh[6 * w + 3] = n;
@@ -456,8 +461,17 @@ __global__ void __launch_bounds__(NT, 2)
         g0 = static_cast<long long>(p.units) * piece / pieces;
         g1 = static_cast<long long>(p.units) * (piece + 1) / pieces;
         __syncthreads();  // barriers initialised
-        if (p.n == 0 && p.row == 0 && piece < NW) empty_rows<D>(a, p.r, a.R, cap);
-        if (p.n == 0) return;
+        if (p.n == 0) {
+            if (p.row == 0 && piece < NW) empty_rows<D>(a, p.r, a.R, cap);
+            if (a.whole_rows > 1) {
+                // in step with the cluster to its end, should others have seen a length
+                if (lane < 2) reinterpret_cast<int*>(smem + C::OFF_ENT)[8 * warp + 4 * lane] = -1;
+                __syncthreads();
+                cluster_sync();
+                cluster_sync();
+            }
+            return;
+        }
     } else {
         const Work work = locate<D, NT>(a, cta * NW, NW, 1, sh, cta == 0);
         __syncthreads();  // rows found, barriers initialised
@@ -732,8 +746,8 @@ __global__ void __launch_bounds__(NT, 2)
         next_row<D>(a, p);
     }
     // a wait that ran out: what is still in flight lands before the CTA leaves
-    if (!ok) {
-        if (lane == 0 && a.status) atomicOr(a.status, VELOX_STATUS_TIMEOUT);
+    if (!ok || ahead > 0) {
+        if (!ok && lane == 0 && a.status) atomicOr(a.status, VELOX_STATUS_TIMEOUT);
         volatile int never = 0;
         for (; ahead > 0; --ahead) {
             if (!mbar_wait(bars + 8 * slot, parity, &never, WAIT_LIMIT_NS)) break;

@@ -491,6 +491,8 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  *   ws  scratch of velox_paged_attn_workspace_size bytes (256-B aligned); may be
  *       NULL (ws_bytes 0) for short histories of few rows: where for an n of 1, 2, 4 or
  *       8, max_pages * page <= 512 n and R * Hkv * ceil(H / Hkv / 16) * n <= 256
+ * table and lens must not change during the call: results are then undefined (what is read
+ * and written stays within the arguments).
  * A request of length 0 gets zeros, with lse = -inf. What lies in a page behind the
  * last token may be anything, NaN too. Scores and softmax statistics are
  * float32; probabilities enter the tensor-core product as the sum of two bf16.
