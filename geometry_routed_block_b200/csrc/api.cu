@@ -332,25 +332,27 @@ int paged_plan_check(const void* a, const void* b, const void* c, const void* d,
     return VELOX_OK;
 }
 
-// Checks and launch of the one-token attention.
+// Checks and launch of the one-token attention. cu (may be null) and N: the rows of q.
 int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
-                   const int32_t* lens, int R, int H, int Hkv, int d, int page, int num_pages,
-                   int max_pages, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
-                   int32_t* status, unsigned long long wait_ns, int skip_warps, void* stream) {
+                   const int32_t* lens, const int32_t* cu, int R, int N, int H, int Hkv, int d,
+                   int page, int num_pages, int max_pages, float scale, void* o, float* lse,
+                   void* ws, size_t ws_bytes, int32_t* status, unsigned long long wait_ns,
+                   int skip_warps, void* stream) {
     if (!q || !k_pages || !v_pages || !table || !lens || !o) return VELOX_EINVAL;
-    if (R < 1 || R > 65535 || Hkv < 1 || H < Hkv || H % Hkv || d < 1 || page < 1 ||
+    if (R < 1 || R > 65535 || N < 1 || Hkv < 1 || H < Hkv || H % Hkv || d < 1 || page < 1 ||
         num_pages < 1 || max_pages < 1)
         return VELOX_EINVAL;
     if (!tile_ok(d) || !page_ok(page)) return VELOX_EUNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
-        !aligned(ws, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+        !aligned(ws, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4) ||
+        !aligned(cu, 4))
         return VELOX_EINVAL;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return VELOX_EINVAL;
     // in this order no product leaves 63 bits
     if (static_cast<long long>(max_pages) * page >= INT_LIMIT ||
         static_cast<long long>(num_pages) * page >= INT_LIMIT ||
         static_cast<long long>(num_pages) * page * Hkv >= INT_LIMIT ||
-        static_cast<long long>(R) * H >= INT_LIMIT)
+        static_cast<long long>(R) * H >= INT_LIMIT || static_cast<long long>(N) * H >= INT_LIMIT)
         return VELOX_EINVAL;
     if (!velox::paged_attn_whole(R, H, Hkv, page, max_pages) &&
         (!ws || ws_bytes < velox::paged_attn_ws_bytes(R, H, Hkv, d)))
@@ -360,6 +362,8 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.table = table;
     a.lens = lens;
+    a.cu = cu;
+    a.N = N;
     a.R = R;
     a.H = H;
     a.Hkv = Hkv;
@@ -577,8 +581,20 @@ int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, co
                      const int32_t* lens, int R, int H, int Hkv, int d, int page, int num_pages,
                      int max_pages, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
                      int32_t* status, void* stream) {
-    return paged_attn_run(q, k_pages, v_pages, table, lens, R, H, Hkv, d, page, num_pages, max_pages,
-                          scale, o, lse, ws, ws_bytes, status, velox::WAIT_LIMIT_NS, 0, stream);
+    return paged_attn_run(q, k_pages, v_pages, table, lens, nullptr, R, R, H, Hkv, d, page, num_pages,
+                          max_pages, scale, o, lse, ws, ws_bytes, status, velox::WAIT_LIMIT_NS, 0,
+                          stream);
+}
+
+int velox_paged_attn_step(const void* q, const void* k_pages, const void* v_pages,
+                          const int32_t* table, const int32_t* lens, const int32_t* cu, int R, int N,
+                          int H, int Hkv, int d, int page, int num_pages, int max_pages, float scale,
+                          void* o, float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                          void* stream) {
+    if (!cu) return VELOX_EINVAL;
+    return paged_attn_run(q, k_pages, v_pages, table, lens, cu, R, N, H, Hkv, d, page, num_pages,
+                          max_pages, scale, o, lse, ws, ws_bytes, status, velox::WAIT_LIMIT_NS, 0,
+                          stream);
 }
 
 int velox_paged_attn_test(const void* q, const void* k_pages, const void* v_pages,
@@ -588,8 +604,8 @@ int velox_paged_attn_test(const void* q, const void* k_pages, const void* v_page
                           int skip_warps, void* stream) {
     if (!(wait_limit_s >= 1e-3 && wait_limit_s <= 10.0)) return VELOX_EINVAL;
     if (skip_warps < 0 || skip_warps > 15) return VELOX_EINVAL;
-    return paged_attn_run(q, k_pages, v_pages, table, lens, R, H, Hkv, d, page, num_pages, max_pages,
-                          scale, o, lse, ws, ws_bytes, status,
+    return paged_attn_run(q, k_pages, v_pages, table, lens, nullptr, R, R, H, Hkv, d, page, num_pages,
+                          max_pages, scale, o, lse, ws, ws_bytes, status,
                           static_cast<unsigned long long>(wait_limit_s * 1e9), skip_warps, stream);
 }
 

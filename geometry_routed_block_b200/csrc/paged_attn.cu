@@ -132,13 +132,36 @@ __device__ __forceinline__ int Work::cta_of(long long u) const {
 
 __device__ __forceinline__ int weight(int units) { return units > 0 ? units + ROW_COST : 0; }
 
+// The row of q and o that request r attends with: its own number or, in a plan's STEP, that
+// of its last new token, -1 where it has none (`bad`: where there can be no such row). STEP is
+// a parameter of the kernels: asked at run time it cost calls without a plan 0.1 to 0.4 us.
+template <bool STEP>
+__device__ __forceinline__ int token_row(const PagedAttnArgs& a, int r, bool& bad) {
+    if (!STEP) return r;
+    const int begin = a.cu[r], end = a.cu[r + 1];
+    const bool there = begin >= 0 && begin < end && end <= a.N;
+    bad |= !there && begin != end;
+    return there ? end - 1 : -1;
+}
+// the same for a request that has one (within q, should cu change meanwhile)
+template <bool STEP>
+__device__ __forceinline__ int row_of(const PagedAttnArgs& a, int r) {
+    return STEP ? min(max(a.cu[r + 1] - 1, 0), a.N - 1) : r;
+}
+// the tokens that request r attends to: none where it has no row
+template <bool STEP>
+__device__ __forceinline__ int tokens_of(const PagedAttnArgs& a, int r, int cap) {
+    bool bad = false;
+    return token_row<STEP>(a, r, bad) < 0 ? 0 : clamp_len(a.lens[r], cap);
+}
+
 // Every thread of the CTA calls it. Counts the work, and finds the rows in which
 // `count` warp shares begin, those numbered first, first + step, ...: sh[6 i] onwards
 // gets the i-th's row (nothing where there is no such share, or an empty one at the
 // end). sh: 6 long longs per share, and one per warp at least. The caller lets the
 // CTA meet before it reads sh. Lengths beyond KEPT a thread are looked at twice: should one
 // change meanwhile, what is found is meaningless, but lies within the arguments.
-template <int D, int THREADS>
+template <int D, bool STEP, int THREADS>
 __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int count, int step,
                                        long long* sh, bool report) {
     const int rows = a.Hkv * a.head_tiles, cap = a.max_pages * a.page;
@@ -151,6 +174,10 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
 #pragma unroll
     for (int i = 0; i < KEPT; ++i)
         if (r0 + i < r1) kept[i] = a.lens[r0 + i];
+    if (STEP)
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i)
+            if (r0 + i < r1 && token_row<STEP>(a, r0 + i, bad) < 0) kept[i] = 0;
 #pragma unroll
     for (int i = 0; i < KEPT; ++i) {
         bad |= kept[i] < 0 || kept[i] > cap;
@@ -158,7 +185,7 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
         mine += weight(units_of<D>(kept[i]));
     }
     for (int r = r0 + KEPT; r < r1; ++r) {
-        const int n = a.lens[r];
+        const int n = token_row<STEP>(a, r, bad) < 0 ? 0 : a.lens[r];
         bad |= n < 0 || n > cap;
         mine += weight(units_of<D>(clamp_len(n, cap)));
     }
@@ -200,7 +227,7 @@ __device__ __forceinline__ Work locate(const PagedAttnArgs& a, int first, int co
             else at = next;
         }
         for (int i = r0 + KEPT; r < 0 && i < r1; ++i) {
-            n = clamp_len(a.lens[i], cap);
+            n = tokens_of<STEP>(a, i, cap);
             const long long next = at + static_cast<long long>(weight(units_of<D>(n))) * rows;
             if (s < next) r = i;
             else at = next;
@@ -230,14 +257,14 @@ __device__ __forceinline__ Row located(const long long* sh) {
 }
 
 // the next row that has units (the caller knows that there is one)
-template <int D>
+template <int D, bool STEP>
 __device__ __forceinline__ void next_row(const PagedAttnArgs& a, Row& p) {
     p.base += weight(p.units);
     if (++p.row < a.Hkv * a.head_tiles) return;
     p.row = 0;
     do {
         ++p.r;
-        p.n = p.r < a.R ? clamp_len(a.lens[p.r], a.max_pages * a.page) : 1;
+        p.n = p.r < a.R ? tokens_of<STEP>(a, p.r, a.max_pages * a.page) : 1;
     } while (p.n == 0);
     p.r = min(p.r, a.R - 1);  // reached only if the lengths change meanwhile: stay within the table
     p.units = units_of<D>(p.n);
@@ -289,18 +316,19 @@ __device__ __forceinline__ float log_sum(float m, float l) {
     return ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
 }
 
-// zeros for the requests r, r + step, ... that have no tokens
-template <int D>
+// zeros for the requests r, r + step, ... that have a row but no tokens
+template <int D, bool STEP>
 __device__ __forceinline__ void empty_rows(const PagedAttnArgs& a, int r, int step, int cap) {
     const int elems = a.H * D;
     for (; r < a.R; r += step) {
         if (clamp_len(a.lens[r], cap) > 0) continue;
+        bool bad = false;
+        const long long row = token_row<STEP>(a, r, bad);
+        if (row < 0) continue;
         for (int i = threadIdx.x; i < elems / 8; i += NT)
-            reinterpret_cast<uint4*>(a.o + static_cast<long long>(r) * elems)[i] =
-                make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(a.o + row * elems)[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
-            for (int h = threadIdx.x; h < a.H; h += NT)
-                a.lse[static_cast<long long>(r) * a.H + h] = -INFINITY;
+            for (int h = threadIdx.x; h < a.H; h += NT) a.lse[row * a.H + h] = -INFINITY;
     }
 }
 
@@ -376,7 +404,7 @@ __device__ __forceinline__ float4 peer_f4(uint32_t addr) {
 
 // The row of a cluster: every CTA joins its warps' parts, then each takes some of the
 // heads' columns and reads the others' results from their shared memory.
-template <int D, int MT>
+template <int D, int MT, bool STEP>
 __device__ __forceinline__ void join_cluster(const PagedAttnArgs& a, uint8_t* smem, const Row& p,
                                              uint32_t entries) {
     using C = Cfg<D, MT>;
@@ -392,7 +420,8 @@ __device__ __forceinline__ void join_cluster(const PagedAttnArgs& a, uint8_t* sm
     cluster_sync();
     const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
     const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
-    const long long q_row = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
+    const long long q_row =
+        static_cast<long long>(row_of<STEP>(a, p.r)) * a.H + hk * a.group + ht * a.tile_heads;
     const int n = a.whole_rows;
     for (int i = cluster_ctarank() * NT + threadIdx.x; i < heads * (D / 4); i += n * NT) {
         const int h = i / (D / 4), col = 4 * (i % (D / 4));
@@ -411,7 +440,7 @@ __device__ __forceinline__ void join_cluster(const PagedAttnArgs& a, uint8_t* sm
     cluster_sync();  // the others have read this CTA's shared memory
 }
 
-template <int D, int MT>
+template <int D, int MT, bool STEP>
 __global__ void __launch_bounds__(NT, 2)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
@@ -452,17 +481,19 @@ __global__ void __launch_bounds__(NT, 2)
         p.base = 0;
         p.r = row / rows;
         p.row = row - p.r * rows;
-        const int n = a.lens[p.r];
+        bool bad = false;
+        const int n = token_row<STEP>(a, p.r, bad) < 0 ? 0 : a.lens[p.r];
         p.n = clamp_len(n, cap);
         p.units = units_of<D>(p.n);
-        if (p.row == 0 && threadIdx.x == 0 && n != p.n && a.status)
+        bad |= n != p.n;
+        if (p.row == 0 && threadIdx.x == 0 && bad && a.status)
             atomicOr(a.status, VELOX_STATUS_BAD_INDEX);
         const int pieces = a.whole_rows * NW;
         g0 = static_cast<long long>(p.units) * piece / pieces;
         g1 = static_cast<long long>(p.units) * (piece + 1) / pieces;
         __syncthreads();  // barriers initialised
         if (p.n == 0) {
-            if (p.row == 0 && piece < NW) empty_rows<D>(a, p.r, a.R, cap);
+            if (p.row == 0 && piece < NW) empty_rows<D, STEP>(a, p.r, a.R, cap);
             if (a.whole_rows > 1) {
                 // in step with the cluster to its end, should others have seen a length
                 if (lane < 2) reinterpret_cast<int*>(smem + C::OFF_ENT)[8 * warp + 4 * lane] = -1;
@@ -473,10 +504,10 @@ __global__ void __launch_bounds__(NT, 2)
             return;
         }
     } else {
-        const Work work = locate<D, NT>(a, cta * NW, NW, 1, sh, cta == 0);
+        const Work work = locate<D, STEP, NT>(a, cta * NW, NW, 1, sh, cta == 0);
         __syncthreads();  // rows found, barriers initialised
         if (cta >= work.grid || work.total == 0) {
-            empty_rows<D>(a, cta, gridDim.x, cap);
+            empty_rows<D, STEP>(a, cta, gridDim.x, cap);
             return;
         }
         g0 = work.start(cta * NW + warp), g1 = work.start(cta * NW + warp + 1);
@@ -506,7 +537,7 @@ __global__ void __launch_bounds__(NT, 2)
             if (f.base + weight(f.units) >= g1) {
                 more = false;
             } else {
-                next_row<D>(a, f);
+                next_row<D, STEP>(a, f);
                 fu = 0;
                 fend = static_cast<int>(min(g1 - f.base, static_cast<long long>(f.units)));
                 ids_at = -32;
@@ -557,7 +588,7 @@ __global__ void __launch_bounds__(NT, 2)
             ++ahead;
         }
 
-    if (!a.whole_rows) empty_rows<D>(a, cta, gridDim.x, cap);  // while the loads are on their way
+    if (!a.whole_rows) empty_rows<D, STEP>(a, cta, gridDim.x, cap);  // while the loads are on their way
 
     const int g = lane >> 2, t = lane & 3;
     int* ent = reinterpret_cast<int*>(smem + C::OFF_ENT) + 8 * warp;  // this warp's two parts
@@ -574,7 +605,7 @@ __global__ void __launch_bounds__(NT, 2)
             const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
             const int head0 = hk * a.group + ht * a.tile_heads;
             const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
-            const long long q_row = static_cast<long long>(p.r) * a.H + head0;
+            const long long q_row = static_cast<long long>(row_of<STEP>(a, p.r)) * a.H + head0;
 
             float o[MT][D / 8][4];
             float m[MT], l[MT];
@@ -743,7 +774,7 @@ __global__ void __launch_bounds__(NT, 2)
             }
         }
         if (p.base + weight(p.units) >= g1) break;
-        next_row<D>(a, p);
+        next_row<D, STEP>(a, p);
     }
     // a wait that ran out: what is still in flight lands before the CTA leaves
     if (!ok || ahead > 0) {
@@ -764,7 +795,7 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
     for (int e = 0; e < 2 * NW; ++e) left |= (ents[4 * e] >= 0 ? 1u : 0u) << e;
     if (clustered) {
-        join_cluster<D, MT>(a, smem, p, left);
+        join_cluster<D, MT, STEP>(a, smem, p, left);
         return;
     }
     while (left) {
@@ -777,7 +808,7 @@ __global__ void __launch_bounds__(NT, 2)
         const int hk = row / a.head_tiles, ht = row - hk * a.head_tiles;
         const int heads = min(a.tile_heads, a.group - ht * a.tile_heads);
         const long long q_row =
-            static_cast<long long>(r) * a.H + hk * a.group + ht * a.tile_heads;
+            static_cast<long long>(row_of<STEP>(a, r)) * a.H + hk * a.group + ht * a.tile_heads;
         float* part = a.part + static_cast<long long>(2 * cta + (begins ? 1 : 0)) * C::PART;
         Joined<D, MT> j;
         join_entries<D, MT>(smem, these, j);
@@ -805,7 +836,7 @@ __global__ void __launch_bounds__(NT, 2)
 // the i-th. Where there are more heads than shares (few parts each), a warp joins a
 // head alone; where there are more shares (many parts), the CTA's warps take parts
 // of one head in turn and meet in shared memory. The order of the sums is fixed.
-template <int D, int MT>
+template <int D, int MT, bool STEP>
 __global__ void __launch_bounds__(JT)
     paged_join_kernel(const __grid_constant__ PagedAttnArgs a) {
     using C = Cfg<D, MT>;
@@ -815,7 +846,7 @@ __global__ void __launch_bounds__(JT)
     __shared__ float red_m[JW], red_l[JW];
     __shared__ float4 red_o[JW][LANES];
     const int c = blockIdx.x;
-    const Work work = locate<D, JT>(a, c * NW, 2, NW, sh, false);
+    const Work work = locate<D, STEP, JT>(a, c * NW, 2, NW, sh, false);
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the row that share c goes on with, and the one it begins and leaves. All of this
@@ -836,7 +867,8 @@ __global__ void __launch_bounds__(JT)
             n[side] = work.cta_of(end - 1) - first[side] + 1;
             const int hk = p.row / a.head_tiles, ht = p.row - hk * a.head_tiles;
             heads[side] = min(a.tile_heads, a.group - ht * a.tile_heads);
-            q_row[side] = static_cast<long long>(p.r) * a.H + hk * a.group + ht * a.tile_heads;
+            q_row[side] =
+                static_cast<long long>(row_of<STEP>(a, p.r)) * a.H + hk * a.group + ht * a.tile_heads;
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -953,7 +985,7 @@ int ctas_per_row(const PagedAttnArgs& a, long long rows) {
     return 0;
 }
 
-template <int D, int MT>
+template <int D, int MT, bool STEP>
 int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream_t st) {
     using C = Cfg<D, MT>;
     static_assert(C::SMEM + 1024 <= 233472 / 2, "shared memory of two CTAs");
@@ -978,7 +1010,7 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     // units in flight: as many as come nearest to IN_FLIGHT bytes on the whole GPU
     const double per_stage = static_cast<double>(a.grid) * NW * C::STAGE;
     a.stages = std::max(2, std::min(C::ST, static_cast<int>(IN_FLIGHT / per_stage + 0.5)));
-    auto kern = paged_attn_kernel<D, MT>;
+    auto kern = paged_attn_kernel<D, MT, STEP>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
         return VELOX_ECUDA;
@@ -1007,7 +1039,7 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     if (a.whole_rows || a.grid == 1) return VELOX_OK;  // no row is shared between shares
     cfg.blockDim = dim3(JT);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, MT>, a) == cudaSuccess ? VELOX_OK
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, MT, STEP>, a) == cudaSuccess ? VELOX_OK
                                                                                : VELOX_ECUDA;
 }
 
@@ -1035,10 +1067,13 @@ int paged_attn_launch(const void* k_pages, const void* v_pages, const PagedAttnA
     a.head_tiles = (a.group + 15) / 16;
     a.whole_rows = paged_attn_whole(a.R, a.H, a.Hkv, a.page, a.max_pages);
     a.tile_heads = (a.group + a.head_tiles - 1) / a.head_tiles;
-    const bool wide = a.group > 8;
+    const bool wide = a.group > 8, step = a.cu != nullptr;
+    const auto run = [&](auto kernel) { return kernel(k_pages, v_pages, a, st); };
     if (d == 128)
-        return wide ? launch<128, 2>(k_pages, v_pages, a, st) : launch<128, 1>(k_pages, v_pages, a, st);
-    return wide ? launch<64, 2>(k_pages, v_pages, a, st) : launch<64, 1>(k_pages, v_pages, a, st);
+        return step ? run(wide ? launch<128, 2, true> : launch<128, 1, true>)
+                    : run(wide ? launch<128, 2, false> : launch<128, 1, false>);
+    return step ? run(wide ? launch<64, 2, true> : launch<64, 1, true>)
+                : run(wide ? launch<64, 2, false> : launch<64, 1, false>);
 }
 
 }  // namespace velox

@@ -135,6 +135,8 @@ struct PagedAttnArgs {
     int32_t* status;
     unsigned long long wait_ns;  // limit of every bounded wait
     int skip_warps;              // test hook: bit w: warp w of every CTA fetches nothing
+    int N;                       // rows of q and o
+    const int32_t* cu;  // [R + 1]: first new token of each request; null: request r has row r
 };
 // CTAs per row where histories are so short that rows are not dealt out by length, and no
 // workspace is needed; else 0

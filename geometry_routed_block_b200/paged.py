@@ -8,7 +8,8 @@ the library calls:
 
 - plan(add): pages and slots for the step's new tokens, once per step;
 - append(layer, plan, ...): rotary positions, and keys and values into their slots;
-- attend(layer, q): the new token of each request against its pages;
+- attend(layer, q, plan=plan): the new token of each request against its pages, in the
+  plan's rows as append returns them; requests without one are idle and skipped;
 - release(done): the pages of finished requests go back.
 
 All state lives on the device and nothing is read back, so a step can be
@@ -73,10 +74,16 @@ class PagedCache:
         return vx.paged_append(k, v, plan.slots, self.k[layer], self.v[layer], q=q, pos=pos,
                                out=out, status=self.status, **self.rope)
 
-    def attend(self, layer: int, q: torch.Tensor, out: torch.Tensor | None = None):
-        """q [R,H,d] bf16, a token per request, against everything appended so far."""
+    def attend(self, layer: int, q: torch.Tensor, out: torch.Tensor | None = None,
+               plan: vx.PagedPlan | None = None):
+        """q bf16 against everything appended so far. With the step's plan, q [N,H,d] has the
+        plan's rows (as append returns them), and each request with new tokens attends with
+        the last of them; the other rows stay as they were in out (0 without out). Without a
+        plan, q [R,H,d] has a row for EVERY request, in their order: append's rows are that
+        only in a step in which each request has one new token."""
         return vx.paged_attn(q, self.k[layer], self.v[layer], self.table, self.lens, ws=self.ws,
-                             out=out, want_lse=False, status=self.status)[0]
+                             out=out, want_lse=False, status=self.status,
+                             cu=None if plan is None else plan.cu)[0]
 
     def release(self, done: torch.Tensor) -> None:
         """Requests with done [R] int32 != 0 end: their pages are free again."""

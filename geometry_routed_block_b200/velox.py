@@ -87,6 +87,8 @@ SIGNATURES = {
     "velox_paged_attn_workspace_size": (_c_size, [_c_int] * 4),
     "velox_paged_attn": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size, _vp,
                                                              _vp]),
+    "velox_paged_attn_step": (_c_int, [_vp] * 6 + [_c_int] * 8 + [_c_float, _vp, _vp, _vp, _c_size,
+                                                                  _vp, _vp]),
     "velox_paged_attn_test": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size,
                                                                   _vp, _c_double, _c_int, _vp]),
 }
@@ -698,11 +700,17 @@ def _needs_no_workspace(rows: int, longest: int) -> bool:
 def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
                lens: torch.Tensor, scale: float | None = None, want_lse: bool = True,
                ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
-               lse: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+               lse: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None,
+               cu: torch.Tensor | None = None):
     """One new token per request, q [R,H,d] bf16, against its first lens [R] tokens
     in k_pages / v_pages [num_pages,Hkv,page,d] bf16 by table [R,max_pages] int32
-    -> (O [R,H,d] bf16, lse [R,H] f32 or None). H is a multiple of Hkv."""
-    R, H, d = shape = q.shape
+    -> (O [R,H,d] bf16, lse [R,H] f32 or None). H is a multiple of Hkv.
+
+    With cu [R+1] int32 of a PagedPlan, q [N,H,d] has the rows of that step's tokens, as
+    paged_append returns them: a request with new tokens attends with the last of them,
+    one without is idle. O and lse have the same rows; those that no request attends
+    with stay as they were in out and lse (0 and -inf in tensors allocated here)."""
+    N, H, d = shape = q.shape
     index = q.get_device()
     pq = _arg(q, "q", _BF16, None, index)
     num_pages, Hkv, page, dp = pages = k_pages.shape
@@ -710,17 +718,19 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         raise ValueError(f"q has heads of {d}, the pages of {dp}")
     kp = _arg(k_pages, "k_pages", _BF16, None, index)
     vp = _arg(v_pages, "v_pages", _BF16, pages, index)
-    tr, width = table.shape
-    if tr != R:
-        raise ValueError(f"table must be [{R},max_pages]")
+    R, width = table.shape
+    if cu is None and R != N:
+        raise ValueError(f"table must be [{N},max_pages]")
     pt = _arg(table, "table", _I32, None, index)
     pl = _arg(lens, "lens", _I32, (R,), index)
+    pc = None if cu is None else _arg(cu, "cu", _I32, (R + 1,), index)
     ps = None if status is None else _arg(status, "status", _I32, None, index)
     there = _elsewhere(q, stream)
     if there is not None:
         with there:
-            return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status)
-    if R == 0:
+            return paged_attn(q, k_pages, v_pages, table, lens, scale, want_lse, ws, out, lse, status,
+                              None, cu)
+    if R == 0 or N == 0:
         pw, nw = None, 0
     elif ws is not None:
         pw, nw = _arg(ws, "ws", torch.uint8, None, index), ws.numel()
@@ -730,7 +740,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         ws = paged_attn_workspace(R, H, Hkv, d, q.device)
         pw, nw = ws.data_ptr(), ws.numel()
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if cu is None else torch.zeros_like(q)
         po = out.data_ptr()
     else:
         po = _arg(out, "out", _BF16, shape, index)
@@ -739,15 +749,20 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     if not want_lse:
         lse = pe = None
     elif lse is None:
-        lse = q.new_empty((R, H), dtype=_F32)
+        lse = q.new_empty((N, H), dtype=_F32) if cu is None else q.new_full((N, H), -math.inf, dtype=_F32)
         pe = lse.data_ptr()
     else:
-        pe = _arg(lse, "lse", _F32, (R, H), index)
-    if R == 0:
-        return out, lse  # no requests
-    _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width,
-                                1.0 / math.sqrt(d) if scale is None else float(scale), po, pe, pw,
-                                nw, ps, _raw_stream(index)), "velox_paged_attn")
+        pe = _arg(lse, "lse", _F32, (N, H), index)
+    if R == 0 or N == 0:
+        return out, lse  # no requests, or no tokens
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if cu is None:
+        _check(lib.velox_paged_attn(pq, kp, vp, pt, pl, R, H, Hkv, d, page, num_pages, width, scale,
+                                    po, pe, pw, nw, ps, _raw_stream(index)), "velox_paged_attn")
+    else:
+        _check(lib.velox_paged_attn_step(pq, kp, vp, pt, pl, pc, R, N, H, Hkv, d, page, num_pages, width,
+                                         scale, po, pe, pw, nw, ps, _raw_stream(index)),
+               "velox_paged_attn_step")
     return out, lse
 
 

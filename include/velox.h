@@ -515,6 +515,25 @@ VELOX_API int velox_paged_attn(const void* q, const void* k_pages, const void* v
                                void* stream);
 
 /*
+ * velox_paged_attn for the rows of a planned step, as velox_paged_append returns them.
+ *   cu [R + 1] int32  velox_paged_plan's: request r's new tokens are rows cu[r] .. cu[r+1] - 1
+ *   q, o [N][H][d] bf16, lse [N][H]
+ * A request with new tokens attends with the last of them, row cu[r+1] - 1, to its first
+ * lens[r] tokens. A request without any is idle: its length, table and pages are not looked
+ * at. Rows of o and lse that no request attends with (padding, all but the last of several
+ * new tokens) are left as they were. A request whose rows are not within [0, N), or end
+ * before they begin, is left out and sets VELOX_STATUS_BAD_INDEX; where cu gives several
+ * requests one row, what that row holds is undefined.
+ * Other arguments, limits and errors as velox_paged_attn; VELOX_EINVAL also for NULL or
+ * misaligned cu, N < 1 or N * H >= 2^31.
+ */
+VELOX_API int velox_paged_attn_step(const void* q, const void* k_pages, const void* v_pages,
+                                    const int32_t* table, const int32_t* lens, const int32_t* cu,
+                                    int R, int N, int H, int Hkv, int d, int page, int num_pages,
+                                    int max_pages, float scale, void* o, float* lse, void* ws,
+                                    size_t ws_bytes, int32_t* status, void* stream);
+
+/*
  * Test entry point: velox_paged_attn with a chosen limit for its bounded waits (1e-3 to
  * 10 s; the copies in flight are waited for with the default limit) and, bit w of
  * skip_warps (0 to 15), without the loads of warp w of every CTA, whose wait then runs

@@ -27,3 +27,34 @@ def test_attn_test_entry_rejects(vx):  # noqa: F811
     rejects(call, -1, ws=None)
     if not torch.cuda.is_available():
         assert call(limit=1e-3, skip=15) == OK_PAST_CHECKS
+
+
+def test_attn_step_rejects(vx):  # noqa: F811
+    def call(cu=FAKE, N=3, **kw):
+        a = attn_args(**kw)
+        return vx.lib.velox_paged_attn_step(*a[:5], cu, a[5], N, *a[6:], None)
+
+    rejects(call, -1, cu=None)
+    rejects(call, -1, cu=OFF2)
+    rejects(call, -1, N=0)
+    rejects(call, -1, N=2**28)          # 2^31 rows of heads
+    rejects(call, -1, R=65536)
+    rejects(call, -1, lens=None)
+    rejects(call, -2, d=32)
+    if not torch.cuda.is_available():
+        assert call() == OK_PAST_CHECKS
+        assert call(N=1) == OK_PAST_CHECKS
+
+
+def test_binding_refuses_rows_that_are_not_the_requests(vx):  # noqa: F811
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    pages = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="table"):
+        vx.paged_attn(q, pages, pages, i(2, 4), i(2))          # three rows, two requests, no plan
+    with pytest.raises(ValueError, match="cu"):
+        vx.paged_attn(q, pages, pages, i(2, 4), i(2), cu=i(2))
+    with pytest.raises(TypeError, match="cu"):
+        vx.paged_attn(q, pages, pages, i(2, 4), i(2), cu=i(3).long())
+    with pytest.raises(ValueError, match="CUDA"):
+        vx.paged_attn(q, pages, pages, i(2, 4), i(2), cu=i(3))
