@@ -438,16 +438,20 @@ def _apart(x: torch.Tensor, y: torch.Tensor) -> bool:
         return True
     if x.dtype != y.dtype or x.shape != y.shape or x.stride() != y.stride() or (c - a) % x.element_size():
         return False
-    # a shared element is an index difference (di, dj, ..., e) that makes up for the offset
+    # a shared element is an index difference (di, dj, ...) that makes up for the offset. From
+    # the largest stride down, only those count that the smaller ones (`rest`) can make up
+    # for: at most two of a dimension that the smaller ones do not reach beyond
+    dims = sorted((st, n) for n, st in zip(x.shape, x.stride()) if n > 1 and st > 0)
+    rests = [0]
+    for st, n in dims:
+        rests.append(rests[-1] + (n - 1) * st)
     reach = {(c - a) // x.element_size()}
-    for n, st in sorted(zip(x.shape, x.stride()), key=lambda p: -p[1])[:-1]:
-        left = {r - i * st for r in reach for i in range(-n + 1, n)}
-        # what the smaller dimensions can still make up for
-        rest = sum((m - 1) * s2 for m, s2 in zip(x.shape, x.stride()) if s2 < st)
-        reach = {r for r in left if abs(r) <= rest}
+    for (st, n), rest in zip(reversed(dims), reversed(rests[:-1])):
+        reach = {r - i * st for r in reach
+                 for i in range(max(-((rest - r) // st), 1 - n), min((r + rest) // st, n - 1) + 1)}
         if len(reach) > 4096:
             return False
-    return all(abs(r) >= x.shape[-1] for r in reach)
+    return 0 not in reach
 
 
 def _in_dtype(t: torch.Tensor, name: str) -> int:

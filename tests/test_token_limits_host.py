@@ -1,6 +1,9 @@
 """Limits of the token calls that are checked before anything is launched, without a GPU."""
 import ctypes
+import math
+import time
 
+import numpy as np
 import pytest
 import torch
 
@@ -58,3 +61,35 @@ def test_binding_refuses_rows_that_are_not_the_requests(vx):  # noqa: F811
         vx.paged_attn(q, pages, pages, i(2, 4), i(2), cu=i(3).long())
     with pytest.raises(ValueError, match="CUDA"):
         vx.paged_attn(q, pages, pages, i(2, 4), i(2), cu=i(3))
+
+
+def test_sibling_slices_are_told_apart_at_once(vx):  # noqa: F811
+    """An output on the sibling slice of a fused projection, as rope(out=) checks it in every
+    call: the time does not grow with the tokens (it did, to 25 ms at 46,080)."""
+    heads, d = 4, 8
+    for tokens in (46_080, 300_000):
+        wide = torch.empty(1, tokens, 3 * heads, d, dtype=torch.bfloat16)
+        q, k = (wide[:, :, i * heads:(i + 1) * heads].transpose(1, 2) for i in range(2))
+        best = math.inf
+        for _ in range(7):
+            t = time.perf_counter()
+            assert vx._apart(q, k)
+            best = min(best, time.perf_counter() - t)
+        assert best < 1e-3
+        assert not vx._apart(q, wide[:, :, 1:heads + 1].transpose(1, 2))
+
+
+def test_shared_elements_of_any_strides(vx):  # noqa: F811
+    """_apart against the sets of addresses: strides that nest or do not, broadcast dimensions."""
+    rng = np.random.default_rng(1)
+    buf = torch.zeros(6000, dtype=torch.float32)
+    count = {True: 0, False: 0}
+    for _ in range(3000):
+        shape = tuple(int(i) for i in rng.integers(1, 6, 3)) + (int(rng.integers(1, 6)),)
+        s = tuple(int(i) for i in rng.choice([0, 1, 2, 3, 5, 6, 7, 12, 30, 31, 64, 200], 3)) + (1,)
+        x, y = (buf.as_strided(shape, s, int(rng.integers(0, 400))) for _ in range(2))
+        at = [set(torch.arange(6000).as_strided(shape, s, t.storage_offset()).flatten().tolist()) for t in (x, y)]
+        apart = not (at[0] & at[1])
+        assert vx._apart(x, y) == apart, (shape, s, x.storage_offset(), y.storage_offset())
+        count[apart] += 1
+    assert min(count.values()) > 200
