@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -46,6 +47,11 @@ class _Rope(ctypes.Structure):
     """velox_rope_t"""
     _fields_ = [("freqs", _vp), ("rot", _c_int), ("style", _c_int), ("axes", _c_int),
                 ("sections", _c_int * 3), ("mscale", _c_float), ("inverse", _c_int)]
+
+
+# the same as bytes, which are packed in a third of the time that the structure takes
+_pack_rope = struct.Struct("P6ifi").pack
+assert struct.calcsize("P6ifi") == ctypes.sizeof(_Rope)
 
 
 # name -> (restype, argtypes); mirrors include/velox.h
@@ -468,17 +474,18 @@ def _sections(style: str, sections: tuple):
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
     if not 1 <= len(sections) <= 3 or not all(0 <= n <= 2048 for n in sections):
         raise ValueError("one to three position axes, of 0 to 2048 pairs each")
-    return ROPE_STYLES[style], len(sections), (_c_int * 3)(*map(int, sections))
+    return (ROPE_STYLES[style], len(sections), *map(int, sections), *[0] * (3 - len(sections)))
 
 
 def _rope_spec(freqs: torch.Tensor, style: str, sections, mscale: float, inverse: bool,
-               index: int) -> _Rope:
+               index: int) -> tuple:
+    """A velox_rope_t and its number of axes."""
     if freqs.dim() != 1:
         raise ValueError("freqs is one-dimensional: a frequency per rotated pair")
     n = freqs.shape[0]
-    code, axes, sec = _sections(style, (n,) if sections is None else tuple(sections))
-    return _Rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, code, axes, sec, float(mscale),
-                 1 if inverse else 0)
+    layout = _sections(style, (n,) if sections is None else tuple(sections))
+    return _pack_rope(_arg(freqs, "freqs", _F64, None, index), 2 * n, *layout, mscale,
+                      1 if inverse else 0), layout[1]
 
 
 def _pos_shape(pos: torch.Tensor, axes: int, N: int, B: int | None) -> tuple:
@@ -511,12 +518,12 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
     dense) -> the same shape and type. pos int32 [N] (one axis), [axes,N] or
     [axes,B,N]; freqs [rot/2] float64; sections: pairs of each axis (default: one
     axis). inverse turns back (which is also the gradient of the forward call); out
-    may be x itself."""
+    may be x itself, or share nothing with it; its strides nest."""
     B, H, N, d = shape = x.shape
     index = x.get_device()
     dt = _in_dtype(x, "x")
-    spec = _rope_spec(freqs, style, sections, mscale, inverse, index)
-    p = _arg(pos, "pos", _I32, _pos_shape(pos, spec.axes, N, B), index)
+    spec, axes = _rope_spec(freqs, style, sections, mscale, inverse, index)
+    p = _arg(pos, "pos", _I32, _pos_shape(pos, axes, N, B), index)
     xs = _rows(x, "x")
     there = _elsewhere(x, stream)
     if there is not None:
@@ -531,11 +538,16 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freqs: torch.Tensor, style: str = "
         if (out.data_ptr() != x.data_ptr() or any(
                 n > 1 and i != j for n, i, j in zip(shape, xs, ys))) and not _apart(x, out):
             raise ValueError("out may be x itself, but not share some of its elements")
+        reach = d  # elements up to the last of the smaller dimensions
+        for st, n in sorted((st, n) for st, n in zip(ys, shape) if n > 1 and st > 0):
+            if st < reach:
+                raise ValueError("out lies on itself: some of its rows share elements")
+            reach += (n - 1) * st
     if 0 in shape:
         return out  # nothing to turn
     batched = pos.dim() == 3
     _check(lib.velox_rope(x.data_ptr(), dt, B, H, N, d, _int64s(xs), p, B * N if batched else N,
-                          N if batched else 0, ctypes.byref(spec), out.data_ptr(), _int64s(ys),
+                          N if batched else 0, spec, out.data_ptr(), _int64s(ys),
                           _raw_stream(index)), "velox_rope")
     return out
 
@@ -565,14 +577,30 @@ def _pages_state(lens, table, free_list, free_count, index: int):
             _arg(free_count, "free_count", _I32, (1,), index))
 
 
+def _separate(inputs: tuple, outputs: tuple) -> None:
+    """Refuses int32 outputs that share elements with an input or another output, of which
+    other threads may not have read or written theirs yet. Each is (name, address, elements)."""
+    spans = sorted([(at, n, name, False) for name, at, n in inputs if n] +
+                   [(at, n, name, True) for name, at, n in outputs if n and at])
+    end_in = end_out = 0
+    for at, n, name, written in spans:
+        if at < end_out or (written and at < end_in):
+            raise ValueError(f"{name} must not share elements of the call's other tensors")
+        if written:
+            end_out = at + 4 * n
+        else:
+            end_in = max(end_in, at + 4 * n)
+
+
 def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_list: torch.Tensor,
                free_count: torch.Tensor, page: int, n_cap: int, out: PagedPlan | None = None,
                status: torch.Tensor | None = None, stream=None) -> PagedPlan:
     """Pages for add [R] new tokens of requests with lens [R] cached ones: enters
     them in table [R,max_pages] and returns the step's PagedPlan with room for n_cap
     tokens (all int32). `out` gives the outputs' tensors; its lens and
-    free_count may be the inputs, so that a captured step carries its state on.
-    Tensors allocated here are views of one buffer."""
+    free_count may be the inputs, so that a captured step carries its state on; else
+    the outputs share nothing with one another or the inputs. Tensors allocated here are
+    views of one buffer."""
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pa = _arg(add, "add", _I32, (R,), index)
@@ -598,6 +626,14 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
         oc, os_, op, oq, ol, of = [
             _arg(t, name, _I32, (size,), index) for t, name, size in
             zip(out, PagedPlan._fields, (R + 1, n_cap, n_cap, n_cap, R, 1))]
+        ins, outs = [("add", pa, R), ("free_list", pf, num_pages)], [
+            ("cu", oc, R + 1), ("slots", os_, n_cap), ("pos", op, n_cap), ("req", oq, n_cap),
+            ("lens", ol, R), ("free_count", of, 1), ("table", pt, R * width), ("status", ps, 1)]
+        if ol != pl:
+            ins.append(("lens", pl, R))
+        if of != pc:
+            ins.append(("free_count", pc, 1))
+        _separate(ins, outs)
     _check(lib.velox_paged_plan(pa, pl, pt, pf, pc, R, width, page, num_pages, n_cap, ol, of, oc,
                                 os_, op, oq, ps, _raw_stream(index)), "velox_paged_plan")
     return out
@@ -608,8 +644,8 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                   lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
                   status: torch.Tensor | None = None, stream=None):
     """The pages of the requests with done [R] != 0 go back on free_list (in
-    place); returns (lens, free_count) afterwards. The outputs may be the inputs;
-    those allocated here are views of one buffer."""
+    place); returns (lens, free_count) afterwards. The outputs may be the inputs, else they
+    share nothing with them; those allocated here are views of one buffer."""
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pd = _arg(done, "done", _I32, (R,), index)
@@ -619,15 +655,30 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
         with there:
             return paged_release(done, lens, table, free_list, free_count, page, lens_out,
                                  free_count_out, status)
+    given = lens_out is not None or free_count_out is not None
     if lens_out is None or free_count_out is None:
         a, b = _pieces(lens.new_empty(R + 1), (R, 1))
         lens_out = a if lens_out is None else lens_out
         free_count_out = b if free_count_out is None else free_count_out
-    _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, int(page), num_pages,
-                                   _arg(lens_out, "lens_out", _I32, (R,), index),
-                                   _arg(free_count_out, "free_count_out", _I32, (1,), index), ps,
+    ol = _arg(lens_out, "lens_out", _I32, (R,), index)
+    of = _arg(free_count_out, "free_count_out", _I32, (1,), index)
+    if given:
+        ins = [("done", pd, R), ("table", pt, R * width)]
+        if ol != pl:
+            ins.append(("lens", pl, R))
+        if of != pc:
+            ins.append(("free_count", pc, 1))
+        _separate(ins, [("lens_out", ol, R), ("free_count_out", of, 1), ("free_list", pf, num_pages),
+                        ("status", ps, 1)])
+    _check(lib.velox_paged_release(pd, pl, pt, pf, pc, R, width, int(page), num_pages, ol, of, ps,
                                    _raw_stream(index)), "velox_paged_release")
     return lens_out, free_count_out
+
+
+@functools.lru_cache(maxsize=256)
+def _strides(*strides):
+    """The host arrays of several tensors' strides (None for None)."""
+    return [None if s is None else _int64s(s) for s in strides]
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
@@ -637,10 +688,10 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
                  out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
     """Writes k, v [N,Hkv,d] (bf16 or f32; any strides, the last dimension dense)
     to their slots [N] int32 (negative: padding) of k_pages / v_pages
-    [num_pages,Hkv,page,d] bf16, in place. With freqs (see rope) k and q
-    [N,H,d] are rotated to pos [axes,N] int32 ([N] for one axis) on the way.
-    Returns q as bf16 [N,H,d], or None without q; out may be q itself (bf16 and
-    contiguous)."""
+    [num_pages,Hkv,page,d] bf16, in place; no other tensor lies in these, nor one of them
+    in the other. With freqs (see rope) k and q [N,H,d] are rotated to pos [axes,N] int32
+    ([N] for one axis) on the way. Returns q as bf16 [N,H,d], or None without q; out may
+    be q itself (bf16 and contiguous)."""
     N, Hkv, d = shape = k.shape
     index = k.get_device()
     dt = _in_dtype(k, "k")
@@ -656,22 +707,22 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     if freqs is not None:
         if pos is None:
             raise ValueError("freqs without pos")
-        spec = _rope_spec(freqs, style, sections, mscale, False, index)
-        pp = _arg(pos, "pos", _I32, _pos_shape(pos, spec.axes, N, None), index)
-        spec = ctypes.byref(spec)
+        spec, axes = _rope_spec(freqs, style, sections, mscale, False, index)
+        pp = _arg(pos, "pos", _I32, _pos_shape(pos, axes, N, None), index)
     H, pq, po, qs = 0, None, None, None
     if q is not None:
         H = q.shape[1]
         pq = _arg(q, "q", k.dtype, (N, H, d), index, dense=False)
-        qs = _int64s(_rows(q, "q"))
+        qs = _rows(q, "q")
     elif out is not None:
         raise ValueError("out without q")
-    ks, vs = _int64s(_rows(k, "k")), _int64s(_rows(v, "v"))
+    ks, vs = _rows(k, "k"), _rows(v, "v")
     there = _elsewhere(k, stream)
     if there is not None:
         with there:
             return paged_append(k, v, slots, k_pages, v_pages, q, pos, freqs, style, sections,
                                 mscale, out, status)
+    pk, size = k.data_ptr(), 2 if dt == VELOX_BF16 else 4
     if out is not None:
         po = _arg(out, "out", _BF16, (N, H, d), index)
         same = po == pq and dt == VELOX_BF16 and q.is_contiguous()
@@ -680,10 +731,25 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     elif q is not None:
         out = q.new_empty((N, H, d)) if dt == VELOX_BF16 else q.new_empty((N, H, d), dtype=_BF16)
         po = out.data_ptr()
+    # the pages are written while k, v and q are read: no other tensor reaches into them
+    nbytes, m, h = 2 * k_pages.numel(), N - 1, Hkv - 1
+    ke, ve = kp + nbytes, vp + nbytes
+    ek = pk + (m * ks[0] + h * ks[1] + d) * size
+    ev = pv + (m * vs[0] + h * vs[1] + d) * size
+    shared = (kp < ve and vp < ke or pk < ke and kp < ek or pk < ve and vp < ek
+              or pv < ke and kp < ev or pv < ve and vp < ev)
+    if q is not None:
+        eq = pq + (m * qs[0] + (H - 1) * qs[1] + d) * size
+        eo = po + 2 * N * H * d
+        shared = (shared or pq < ke and kp < eq or pq < ve and vp < eq
+                  or po < ke and kp < eo or po < ve and vp < eo)
+    if shared:
+        raise ValueError("k_pages and v_pages must not share elements with each other or with q, k, v, out")
     if N == 0:
         return out  # no tokens
-    _check(lib.velox_paged_append(pq, k.data_ptr(), pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N,
-                                  spec, po, kp, vp, page, num_pages, ps, _raw_stream(index)),
+    qs, ks, vs = _strides(qs, ks, vs)
+    _check(lib.velox_paged_append(pq, pk, pv, dt, N, H, Hkv, d, qs, ks, vs, psl, pp, N, spec, po, kp, vp,
+                                  page, num_pages, ps, _raw_stream(index)),
            "velox_paged_append")
     return out
 
@@ -748,8 +814,9 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         po = out.data_ptr()
     else:
         po = _arg(out, "out", _BF16, shape, index)
-        if not _apart(q, out):
-            raise ValueError("out must not share elements of q: other parts still read them")
+        nbytes = 2 * k_pages.numel()
+        if not _apart(q, out) or any(po < p + nbytes and po + 2 * N * H * d > p for p in (kp, vp)):
+            raise ValueError("out must not share elements of q or the pages: other parts still read them")
     if not want_lse:
         lse = pe = None
     elif lse is None:
@@ -757,6 +824,10 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
         pe = lse.data_ptr()
     else:
         pe = _arg(lse, "lse", _F32, (N, H), index)
+        nbytes, rows = 2 * k_pages.numel(), 2 * N * H * d
+        if any(pe < p + n and pe + 4 * N * H > p
+               for p, n in ((pq, rows), (po, rows), (kp, nbytes), (vp, nbytes))):
+            raise ValueError("lse must not share elements of q, out or the pages")
     if R == 0 or N == 0:
         return out, lse  # no requests, or no tokens
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)

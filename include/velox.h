@@ -407,7 +407,8 @@ VELOX_API int velox_rope(const void* x, int dtype, int B, int H, int N, int d, c
  *   lens  [R] int32     tokens already cached
  *   table [R][max_pages] int32   the new pages are entered behind the old ones
  *   free_list [num_pages], free_count [1] int32   the free pages (a stack)
- *   lens_out [R], free_count_out [1] int32 outputs; may be lens and free_count
+ *   lens_out [R], free_count_out [1] int32 outputs; may be lens and free_count. Apart from
+ *         that the outputs (table and status among them) share nothing with other arguments
  *   cu    [R + 1] int32 output: request r's new tokens are cu[r] .. cu[r+1] - 1
  *   slots, pos, req [n_cap] int32 outputs: slot, position in its request and
  *         request of each new token, -1 from token cu[R] on; pos and req may be
@@ -460,7 +461,8 @@ VELOX_API int velox_paged_release(const int32_t* done, const int32_t* lens, cons
  *   rope  rotation of q and k, or NULL (none: pos is not read)
  *   q_out [N][H][d] bf16 output (dense; NULL without q): every row is written. It may
  *         be q itself (dense bf16), and shares no element with q, k or v otherwise
- *   k_pages, v_pages [num_pages][Hkv][page][d] bf16; other rows stay as they are
+ *   k_pages, v_pages [num_pages][Hkv][page][d] bf16; other rows stay as they are. They share
+ *         nothing with each other or with the other arguments
  * Everything is rounded to bf16 once, after the rotation. A slot of
  * num_pages * page or more is skipped and sets VELOX_STATUS_BAD_INDEX.
  * Errors: VELOX_EINVAL for non-positive sizes, N, H or Hkv >= 2^31,
@@ -486,8 +488,8 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  *   head h reads key head h / (H / Hkv)
  *   table [R][max_pages], lens [R] int32: request r attends to its first lens[r]
  *   tokens (its new token among them, once appended)
- *   o [R][H][d] bf16 output, which shares nothing with q; lse [R][H] float32 output (natural log of the
- *   softmax denominator of the scaled scores) or NULL
+ *   o [R][H][d] bf16 output; lse [R][H] float32 output (natural log of the softmax
+ *   denominator of the scaled scores) or NULL. They share nothing with the other arguments
  *   ws  scratch of velox_paged_attn_workspace_size bytes (256-B aligned); may be
  *       NULL (ws_bytes 0) for short histories of few rows: where for an n of 1, 2, 4 or
  *       8, max_pages * page <= 512 n and R * Hkv * ceil(H / Hkv / 16) * n <= 256
