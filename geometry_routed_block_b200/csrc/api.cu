@@ -337,7 +337,7 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
                    const int32_t* lens, const int32_t* cu, int R, int N, int H, int Hkv, int d,
                    int page, int num_pages, int max_pages, float scale, void* o, float* lse,
                    void* ws, size_t ws_bytes, int32_t* status, unsigned long long wait_ns,
-                   int skip_warps, void* stream) {
+                   int skip_warps, int most_cluster, void* stream) {
     if (!q || !k_pages || !v_pages || !table || !lens || !o) return VELOX_EINVAL;
     if (R < 1 || R > 65535 || N < 1 || Hkv < 1 || H < Hkv || H % Hkv || d < 1 || page < 1 ||
         num_pages < 1 || max_pages < 1)
@@ -378,6 +378,7 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
     a.status = status;
     a.wait_ns = wait_ns;
     a.skip_warps = skip_warps;
+    a.most_cluster = most_cluster;
     return velox::paged_attn_launch(k_pages, v_pages, a, d, as_stream(stream));
 }
 
@@ -583,7 +584,7 @@ int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages, co
                      int32_t* status, void* stream) {
     return paged_attn_run(q, k_pages, v_pages, table, lens, nullptr, R, R, H, Hkv, d, page, num_pages,
                           max_pages, scale, o, lse, ws, ws_bytes, status, velox::WAIT_LIMIT_NS, 0,
-                          stream);
+                          velox::MAX_CLUSTER, stream);
 }
 
 int velox_paged_attn_step(const void* q, const void* k_pages, const void* v_pages,
@@ -594,19 +595,21 @@ int velox_paged_attn_step(const void* q, const void* k_pages, const void* v_page
     if (!cu) return VELOX_EINVAL;
     return paged_attn_run(q, k_pages, v_pages, table, lens, cu, R, N, H, Hkv, d, page, num_pages,
                           max_pages, scale, o, lse, ws, ws_bytes, status, velox::WAIT_LIMIT_NS, 0,
-                          stream);
+                          velox::MAX_CLUSTER, stream);
 }
 
 int velox_paged_attn_test(const void* q, const void* k_pages, const void* v_pages,
                           const int32_t* table, const int32_t* lens, int R, int H, int Hkv, int d,
                           int page, int num_pages, int max_pages, float scale, void* o, float* lse,
                           void* ws, size_t ws_bytes, int32_t* status, double wait_limit_s,
-                          int skip_warps, void* stream) {
+                          int skip_warps, int most_cluster, void* stream) {
     if (!(wait_limit_s >= 1e-3 && wait_limit_s <= 10.0)) return VELOX_EINVAL;
-    if (skip_warps < 0 || skip_warps > 15) return VELOX_EINVAL;
+    if (skip_warps < 0 || skip_warps > 15 || most_cluster < 1 || most_cluster > velox::MAX_CLUSTER)
+        return VELOX_EINVAL;
     return paged_attn_run(q, k_pages, v_pages, table, lens, nullptr, R, R, H, Hkv, d, page, num_pages,
                           max_pages, scale, o, lse, ws, ws_bytes, status,
-                          static_cast<unsigned long long>(wait_limit_s * 1e9), skip_warps, stream);
+                          static_cast<unsigned long long>(wait_limit_s * 1e9), skip_warps, most_cluster,
+                          stream);
 }
 
 }  // extern "C"

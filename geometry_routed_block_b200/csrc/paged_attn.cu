@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -978,11 +979,41 @@ __global__ void __launch_bounds__(JT)
 // tokens 16.7 and 19.8 us, 32,768 tokens 67.7 and 70.3 us, 225,793 tokens 412 and 407 us
 // (clusters of 8: 16.4, 70.3, 455 us; of 11, which do not fit: 26.2, 103, 610 us). 8 key
 // heads (128 CTAs, not taken): 9.9 and 12.0 us at 4096 tokens, 195 and 148 us at 225,793.
-int ctas_per_row(const PagedAttnArgs& a, long long rows) {
+// places(n): the device can place a cluster of n CTAs, more than the 8 that any can.
+template <typename F>
+int ctas_per_row(const PagedAttnArgs& a, long long rows, F places) {
     if (a.whole_rows || a.R > 1) return a.whole_rows;
     for (const int n : {16, 10, 8})
-        if (rows * n <= 256 && rows * n >= 160) return n;
+        if (rows * n <= 256 && rows * n >= 160 && n <= a.most_cluster && (n <= 8 || places(n)))
+            return n;
     return 0;
+}
+
+// Whether the current device can place a cluster of n of the kernel's CTAs: a part of a GPU may
+// be too small for it. `known` keeps the answer (0: not asked yet, 1: no, 2: yes).
+template <typename K>
+bool can_place(K kern, int n, size_t smem, std::atomic<int>& known) {
+    int answer = known.load(std::memory_order_relaxed);
+    if (answer == 0) {
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = n;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        const bool asked =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess;
+        if (!asked) cudaGetLastError();  // the refusal is the answer, not the call's error
+        answer = asked && clusters > 0 ? 2 : 1;
+        known.store(answer, std::memory_order_relaxed);
+    }
+    return answer == 2;
 }
 
 template <int D, int MT, bool STEP>
@@ -1001,7 +1032,15 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     const int resident = std::min(7 * sms / 4, MAX_GRID);
     const long long rows = static_cast<long long>(a.R) * a.Hkv * a.head_tiles;
     const long long units = static_cast<long long>(a.max_pages) * a.page / C::UNIT + 1;
-    a.whole_rows = ctas_per_row(a, rows);
+    auto kern = paged_attn_kernel<D, MT, STEP>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+        return VELOX_ECUDA;
+    constexpr int DEVICES = 64;  // beyond these no cluster of more than 8 is taken
+    static std::atomic<int> known[DEVICES][2];
+    a.whole_rows = ctas_per_row(a, rows, [&](int n) {
+        return dev < DEVICES && can_place(kern, n, C::SMEM, known[dev][n == 16]);
+    });
     // no more CTAs than the longest histories could keep busy
     a.grid = static_cast<int>(
         a.whole_rows ? rows * a.whole_rows
@@ -1010,10 +1049,6 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     // units in flight: as many as come nearest to IN_FLIGHT bytes on the whole GPU
     const double per_stage = static_cast<double>(a.grid) * NW * C::STAGE;
     a.stages = std::max(2, std::min(C::ST, static_cast<int>(IN_FLIGHT / per_stage + 0.5)));
-    auto kern = paged_attn_kernel<D, MT, STEP>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
-        cudaSuccess)
-        return VELOX_ECUDA;
     if (a.whole_rows > 8 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return VELOX_ECUDA;

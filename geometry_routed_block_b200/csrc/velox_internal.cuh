@@ -14,6 +14,7 @@ namespace velox {
 // default limit of the attention kernels' bounded waits: 2 s, far above any
 // legitimate wait
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;
+constexpr int MAX_CLUSTER = 16;  // CTAs of a cluster
 
 struct AttnArgs {
     const int32_t* idx;  // [B*H][m][n_sel] or nullptr (dense)
@@ -135,6 +136,7 @@ struct PagedAttnArgs {
     int32_t* status;
     unsigned long long wait_ns;  // limit of every bounded wait
     int skip_warps;              // test hook: bit w: warp w of every CTA fetches nothing
+    int most_cluster;            // CTAs of a cluster at most (test hook: fewer than the device's)
     int N;                       // rows of q and o
     const int32_t* cu;  // [R + 1]: first new token of each request; null: request r has row r
 };

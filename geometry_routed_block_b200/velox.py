@@ -96,7 +96,7 @@ SIGNATURES = {
     "velox_paged_attn_step": (_c_int, [_vp] * 6 + [_c_int] * 8 + [_c_float, _vp, _vp, _vp, _c_size,
                                                                   _vp, _vp]),
     "velox_paged_attn_test": (_c_int, [_vp] * 5 + [_c_int] * 7 + [_c_float, _vp, _vp, _vp, _c_size,
-                                                                  _vp, _c_double, _c_int, _vp]),
+                                                                  _vp, _c_double, _c_int, _c_int, _vp]),
 }
 
 
@@ -843,9 +843,10 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
 
 def paged_attn_test(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                     table: torch.Tensor, lens: torch.Tensor, status: torch.Tensor,
-                    wait_limit_s: float, skip_warps: int, ws: torch.Tensor | None = None):
-    """paged_attn through the test entry point (bounded-wait limit, and the warps that fetch
-    nothing); returns (O, lse), undefined where the waits ran out."""
+                    wait_limit_s: float, skip_warps: int, ws: torch.Tensor | None = None,
+                    most_cluster: int = 16):
+    """paged_attn through the test entry point (bounded-wait limit, the warps that fetch
+    nothing, the largest cluster); returns (O, lse), undefined where the waits ran out."""
     R, H, d = q.shape
     num_pages, Hkv, page, _ = k_pages.shape
     _expect(q, _BF16, "q")
@@ -856,5 +857,5 @@ def paged_attn_test(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), R, H, Hkv, d, page, num_pages,
         table.shape[1], 1.0 / math.sqrt(d), _ptr(out), _ptr(lse), _ptr(ws),
         0 if ws is None else ws.numel(), _ptr(status), float(wait_limit_s), int(skip_warps),
-        _stream()), "velox_paged_attn_test")
+        int(most_cluster), _stream()), "velox_paged_attn_test")
     return out, lse

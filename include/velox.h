@@ -539,14 +539,15 @@ VELOX_API int velox_paged_attn_step(const void* q, const void* k_pages, const vo
  * Test entry point: velox_paged_attn with a chosen limit for its bounded waits (1e-3 to
  * 10 s; the copies in flight are waited for with the default limit) and, bit w of
  * skip_warps (0 to 15), without the loads of warp w of every CTA, whose wait then runs
- * out. Not for product use.
+ * out; most_cluster (1 to 16): as on a device that cannot place clusters of more CTAs for a
+ * single request. Not for product use.
  */
 VELOX_API int velox_paged_attn_test(const void* q, const void* k_pages, const void* v_pages,
                                     const int32_t* table, const int32_t* lens, int R, int H,
                                     int Hkv, int d, int page, int num_pages, int max_pages,
                                     float scale, void* o, float* lse, void* ws, size_t ws_bytes,
                                     int32_t* status, double wait_limit_s, int skip_warps,
-                                    void* stream);
+                                    int most_cluster, void* stream);
 
 /*
  * Measurement helper, not a step of the method: blocks x threads threads each

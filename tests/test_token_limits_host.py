@@ -18,13 +18,15 @@ def attn_args(**kw):
 
 
 def test_attn_test_entry_rejects(vx):  # noqa: F811
-    def call(limit=1.0, skip=0, **kw):
-        return vx.lib.velox_paged_attn_test(*attn_args(**kw), limit, skip, None)
+    def call(limit=1.0, skip=0, most=16, **kw):
+        return vx.lib.velox_paged_attn_test(*attn_args(**kw), limit, skip, most, None)
 
     for bad in (0.0, -1.0, 20.0, float("nan"), 1e-4):
         rejects(call, -1, limit=bad)
     for bad in (-1, 16):
         rejects(call, -1, skip=bad)
+    for bad in (0, 17):
+        rejects(call, -1, most=bad)
     rejects(call, -1, q=None)
     rejects(call, -2, page=8)
     rejects(call, -1, ws=None)
