@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const __grid_constant__ 
         a.table[static_cast<long long>(r) * a.max_pages + col] = a.free_list[fc - 1 - p];
     }
     bool stray = false;
-    for (int t = gtid; t < a.n_cap; t += all) {
+    // unsigned: the step behind the last token may pass 2^31
+    for (unsigned i = gtid; i < static_cast<unsigned>(a.n_cap); i += all) {
+        const int t = static_cast<int>(i);
         int slot = -1, pos = -1, r = -1;
         if (t < tokens) {
             r = owner(tok, a.R, t);
