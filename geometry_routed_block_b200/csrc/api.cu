@@ -272,6 +272,8 @@ int velox_cast_bf16(const float* x, uint16_t* y, size_t n, void* stream) {
 namespace {
 
 constexpr long long INT_LIMIT = 1ll << 31;
+// heads of a rotary launch: the kernels count them in 32 bits, a part beyond the last
+constexpr long long MAX_ROWS = 1ll << 30;
 
 inline bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 
@@ -429,7 +431,7 @@ int velox_rope(const void* x, int dtype, int B, int H, int N, int d, const int64
                const velox_rope_t* rope, void* y, const int64_t* ys, void* stream) {
     if (!x || !y || !rope || !xs || !ys) return VELOX_EINVAL;
     if (dtype != VELOX_BF16 && dtype != VELOX_F32) return VELOX_EUNSUPPORTED;
-    if (B < 1 || H < 1 || N < 1 || d < 1 || d > 4096) return VELOX_EINVAL;
+    if (B < 1 || H < 1 || H > MAX_ROWS || N < 1 || d < 1 || d > 4096) return VELOX_EINVAL;
     if (static_cast<long long>(B) * N >= INT_LIMIT) return VELOX_EINVAL;
     const int esize = dtype == VELOX_BF16 ? 2 : 4;
     if (!aligned(x, esize) || !aligned(y, esize)) return VELOX_EINVAL;
@@ -476,7 +478,7 @@ int velox_paged_append(const void* q, const void* k, const void* v, int dtype, i
         return VELOX_EINVAL;
     if (!page_ok(page) || !tile_ok(d)) return VELOX_EUNSUPPORTED;
     const long long n_slots = static_cast<long long>(num_pages) * page;
-    if (n_slots >= INT_LIMIT || static_cast<long long>(q ? H : 0) + 2ll * Hkv >= INT_LIMIT)
+    if (n_slots >= INT_LIMIT || static_cast<long long>(q ? H : 0) + 2ll * Hkv > MAX_ROWS)
         return VELOX_EINVAL;
     const int esize = dtype == VELOX_BF16 ? 2 : 4;
     if (!aligned(k, esize) || !aligned(v, esize) || (q && !aligned(q, esize))) return VELOX_EINVAL;

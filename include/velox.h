@@ -390,7 +390,7 @@ VELOX_API int velox_rope_freqs(int rot, double base, int kind, double factor, in
  *         pos[a * pos_axis_stride + b * pos_batch_stride + n] on axis a
  * Any alignment is taken; rows whose pointers, strides, rot and d allow 16-byte
  * accesses are faster.
- * Errors: VELOX_EINVAL for non-positive sizes, B*N or H >= 2^31, d > 4096,
+ * Errors: VELOX_EINVAL for non-positive sizes, B*N >= 2^31, H > 2^30, d > 4096,
  * negative strides (or 0 in ys along a dimension longer than 1), an inconsistent
  * velox_rope_t (NULL freqs with rot > 0, odd rot or rot > d, axes outside 1..3,
  * sections that do not sum to rot/2, mscale not finite), pointers not aligned to
@@ -465,7 +465,7 @@ VELOX_API int velox_paged_release(const int32_t* done, const int32_t* lens, cons
  *         nothing with each other or with the other arguments
  * Everything is rounded to bf16 once, after the rotation. A slot of
  * num_pages * page or more is skipped and sets VELOX_STATUS_BAD_INDEX.
- * Errors: VELOX_EINVAL for non-positive sizes, N, H or Hkv >= 2^31,
+ * Errors: VELOX_EINVAL for non-positive sizes, H + 2 Hkv > 2^30 (H counted with q),
  * num_pages * page >= 2^31, negative strides, an inconsistent rope (see
  * velox_rope), pages or q_out not 16-byte aligned, inputs not aligned to their
  * element, NULL pointers, q without q_out or the reverse; VELOX_EUNSUPPORTED for

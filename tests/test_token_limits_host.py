@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_token_ops_host import FAKE, OFF2, OK_PAST_CHECKS, rejects, vx  # noqa: F401
+from tests.test_token_ops_host import FAKE, OFF2, OK_PAST_CHECKS, rejects, spec, strides, vx  # noqa: F401
 
 
 def attn_args(**kw):
@@ -95,3 +95,22 @@ def test_shared_elements_of_any_strides(vx):  # noqa: F811
         assert vx._apart(x, y) == apart, (shape, s, x.storage_offset(), y.storage_offset())
         count[apart] += 1
     assert min(count.values()) > 200
+
+
+def test_rotary_heads_whose_counters_would_pass_32_bits_are_refused(vx):  # noqa: F811
+    """A part of the heads ends at first + heads a part, and 8 are taken at a time: neither may
+    pass 2^31."""
+    def rope(H):
+        return vx.lib.velox_rope(FAKE, 0, 1, H, 1, 1, strides(0, 0, 0), None, 1, 0,
+                                 ctypes.byref(spec(vx, rot=0, sections=(0, 0, 0), freqs=None)), FAKE,
+                                 strides(0, 1, 1), None)
+
+    def append(H, Hkv):
+        return vx.lib.velox_paged_append(FAKE, FAKE, FAKE, 0, 1, H, Hkv, 64, strides(64, 64), strides(64, 64),
+                                         strides(64, 64), FAKE, None, 1, None, FAKE, FAKE, FAKE, 16, 8, None,
+                                         None)
+
+    assert rope(2**31 - 1) == -1 and rope(2**30 + 1) == -1
+    assert append(2**30, 1) == -1 and append(1, 2**29) == -1
+    if not torch.cuda.is_available():
+        assert rope(2**30) == OK_PAST_CHECKS and append(2**30 - 2, 1) == OK_PAST_CHECKS
