@@ -349,7 +349,9 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
         !aligned(ws, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4) ||
         !aligned(cu, 4))
         return VELOX_EINVAL;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return VELOX_EINVAL;
+    const float scale_log2 =
+        static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    if (!(scale > 0.0f) || !std::isfinite(scale_log2)) return VELOX_EINVAL;
     // in this order no product leaves 63 bits
     if (static_cast<long long>(max_pages) * page >= INT_LIMIT ||
         static_cast<long long>(num_pages) * page >= INT_LIMIT ||
@@ -373,7 +375,7 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
     a.page_shift = log2_page(page);
     a.num_pages = num_pages;
     a.max_pages = max_pages;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.o = static_cast<__nv_bfloat16*>(o);
     a.lse = lse;
     a.part = static_cast<float*>(ws);

@@ -505,10 +505,10 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  * An expired internal wait sets VELOX_STATUS_TIMEOUT (outputs then undefined; nothing else
  * is written).
  * Errors: VELOX_EINVAL for R < 1 or R > 65535, H < 1, H not a multiple of Hkv,
- * scale not positive and finite, max_pages or num_pages < 1, max_pages * page or
- * num_pages * Hkv * page >= 2^31, R * H >= 2^31, ws_bytes too small, NULL or
- * misaligned (16 B; ws 256 B) pointers; VELOX_EUNSUPPORTED for page not in
- * {16, 32, 64, 128} or d not in {64, 128}.
+ * scale not positive or scale * log2(e) not finite in float32, max_pages or
+ * num_pages < 1, max_pages * page or num_pages * Hkv * page >= 2^31, R * H >= 2^31,
+ * ws_bytes too small, NULL or misaligned (16 B; ws 256 B; int32 and float arrays 4 B)
+ * pointers; VELOX_EUNSUPPORTED for page not in {16, 32, 64, 128} or d not in {64, 128}.
  */
 VELOX_API int velox_paged_attn(const void* q, const void* k_pages, const void* v_pages,
                                const int32_t* table, const int32_t* lens, int R, int H, int Hkv,

@@ -114,3 +114,14 @@ def test_rotary_heads_whose_counters_would_pass_32_bits_are_refused(vx):  # noqa
     assert append(2**30, 1) == -1 and append(1, 2**29) == -1
     if not torch.cuda.is_available():
         assert rope(2**30) == OK_PAST_CHECKS and append(2**30 - 2, 1) == OK_PAST_CHECKS
+
+
+def test_attn_refuses_scales_that_leave_float32(vx):  # noqa: F811
+    """The kernel multiplies scores by scale * log2(e): infinite above 2.36e38, all scores of 0
+    then became NaN."""
+    def call(scale):
+        return vx.lib.velox_paged_attn(*attn_args(scale=scale), None)
+
+    assert call(2.4e38) == -1 and call(3.4e38) == -1
+    if not torch.cuda.is_available():
+        assert call(2.3e38) == OK_PAST_CHECKS
