@@ -347,7 +347,7 @@ int paged_attn_run(const void* q, const void* k_pages, const void* v_pages, cons
     if (!tile_ok(d) || !page_ok(page)) return VELOX_EUNSUPPORTED;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 16) ||
         !aligned(ws, 256) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4) ||
-        !aligned(cu, 4))
+        !aligned(cu, 4) || !aligned(status, 4))
         return VELOX_EINVAL;
     const float scale_log2 =
         static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -485,7 +485,7 @@ int velox_paged_append(const void* q, const void* k, const void* v, int dtype, i
     const int esize = dtype == VELOX_BF16 ? 2 : 4;
     if (!aligned(k, esize) || !aligned(v, esize) || (q && !aligned(q, esize))) return VELOX_EINVAL;
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || (q && !aligned(q_out, 16)) ||
-        !aligned(slots, 4))
+        !aligned(slots, 4) || !aligned(status, 4))
         return VELOX_EINVAL;
     for (int i = 0; i < 2; ++i)
         if (ks[i] < 0 || vs[i] < 0 || (q && qs[i] < 0)) return VELOX_EINVAL;
@@ -533,6 +533,8 @@ int velox_paged_plan(const int32_t* add, const int32_t* lens, int32_t* table,
                                     free_count_out, R, max_pages, page, num_pages);
     if (rc != VELOX_OK) return rc;
     if (!cu || n_cap < 0 || (n_cap > 0 && !slots)) return VELOX_EINVAL;
+    for (const void* p : {cu, slots, pos, req, status})
+        if (!aligned(p, 4)) return VELOX_EINVAL;
     velox::PlanArgs a{};
     a.add = add;
     a.lens = lens;
@@ -561,6 +563,7 @@ int velox_paged_release(const int32_t* done, const int32_t* lens, const int32_t*
     const int rc = paged_plan_check(done, lens, table, free_list, free_count, lens_out,
                                     free_count_out, R, max_pages, page, num_pages);
     if (rc != VELOX_OK) return rc;
+    if (!aligned(status, 4)) return VELOX_EINVAL;
     velox::PlanArgs a{};
     a.add = done;
     a.lens = lens;

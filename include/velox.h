@@ -425,8 +425,8 @@ VELOX_API int velox_rope(const void* x, int dtype, int B, int H, int N, int d, c
  * page id in table or free_list is outside [0, num_pages) gets slot -1 and sets
  * VELOX_STATUS_BAD_INDEX.
  * Errors: VELOX_EINVAL for R outside [1, 8192], n_cap < 0, page, max_pages or
- * num_pages < 1, max_pages * page or num_pages * page >= 2^31, or NULL
- * pointers; VELOX_EUNSUPPORTED for page not in {16, 32, 64, 128}.
+ * num_pages < 1, max_pages * page or num_pages * page >= 2^31, or NULL or
+ * misaligned (4 B) pointers; VELOX_EUNSUPPORTED for page not in {16, 32, 64, 128}.
  */
 VELOX_API int velox_paged_plan(const int32_t* add, const int32_t* lens, int32_t* table,
                                const int32_t* free_list, const int32_t* free_count, int R,
@@ -467,7 +467,7 @@ VELOX_API int velox_paged_release(const int32_t* done, const int32_t* lens, cons
  * num_pages * page or more is skipped and sets VELOX_STATUS_BAD_INDEX.
  * Errors: VELOX_EINVAL for non-positive sizes, H + 2 Hkv > 2^30 (H counted with q),
  * num_pages * page >= 2^31, negative strides, an inconsistent rope (see
- * velox_rope), pages or q_out not 16-byte aligned, inputs not aligned to their
+ * velox_rope), pages or q_out not 16-byte aligned, other arrays not aligned to their
  * element, NULL pointers, q without q_out or the reverse; VELOX_EUNSUPPORTED for
  * page not in {16, 32, 64, 128}, d not in {64, 128}, an unknown dtype or style.
  */

@@ -125,3 +125,31 @@ def test_attn_refuses_scales_that_leave_float32(vx):  # noqa: F811
     assert call(2.4e38) == -1 and call(3.4e38) == -1
     if not torch.cuda.is_available():
         assert call(2.3e38) == OK_PAST_CHECKS
+
+
+def test_misaligned_words_are_refused(vx):  # noqa: F811
+    def plan(**kw):
+        a = dict(add=FAKE, lens=FAKE, table=FAKE, fl=FAKE, fc=FAKE, R=4, mp=8, page=16, np=32, n_cap=8,
+                 lo=FAKE, fo=FAKE, cu=FAKE, slots=FAKE, pos=FAKE, req=FAKE, status=FAKE)
+        return vx.lib.velox_paged_plan(*{**a, **kw}.values(), None)
+
+    def release(**kw):
+        a = dict(done=FAKE, lens=FAKE, table=FAKE, fl=FAKE, fc=FAKE, R=4, mp=8, page=16, np=32, lo=FAKE,
+                 fo=FAKE, status=FAKE)
+        return vx.lib.velox_paged_release(*{**a, **kw}.values(), None)
+
+    def append(**kw):
+        a = dict(q=None, k=FAKE, v=FAKE, dtype=0, N=4, H=0, Hkv=2, d=64, qs=None, ks=strides(128, 64),
+                 vs=strides(128, 64), slots=FAKE, pos=None, pa=0, rope=None, out=None, kp=FAKE, vp=FAKE,
+                 page=16, np=8, status=FAKE)
+        return vx.lib.velox_paged_append(*{**a, **kw}.values(), None)
+
+    def attn(**kw):
+        return vx.lib.velox_paged_attn(*attn_args(**kw), None)
+
+    for name in ("cu", "slots", "pos", "req"):
+        rejects(plan, -1, **{name: OFF2})
+    for call in (plan, release, append, attn):
+        rejects(call, -1, status=OFF2)
+        if not torch.cuda.is_available():
+            assert call() == OK_PAST_CHECKS and call(status=None) == OK_PAST_CHECKS
