@@ -415,6 +415,14 @@ def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None, in
     return t.data_ptr()
 
 
+def _status(t: torch.Tensor, index: int) -> int:
+    """The address of a status word."""
+    at = _arg(t, "status", _I32, None, index)
+    if not at:
+        raise ValueError("status must have an element")
+    return at
+
+
 @functools.lru_cache(maxsize=256)
 def _int64s(values: tuple):
     """A host array the library reads; equal values share one."""
@@ -604,7 +612,7 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pa = _arg(add, "add", _I32, (R,), index)
-    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    ps = None if status is None else _status(status, index)
     page, n_cap = int(page), int(n_cap)
     if not 0 <= n_cap < 2 ** 31:
         raise ValueError("n_cap must be in [0, 2^31)")
@@ -649,7 +657,7 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pd = _arg(done, "done", _I32, (R,), index)
-    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    ps = None if status is None else _status(status, index)
     there = _elsewhere(lens, stream)
     if there is not None:
         with there:
@@ -702,7 +710,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     vp = _arg(v_pages, "v_pages", _BF16, pages, index)
     pv = _arg(v, "v", k.dtype, shape, index, dense=False)
     psl = _arg(slots, "slots", _I32, (N,), index)
-    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    ps = None if status is None else _status(status, index)
     spec = pp = None
     if freqs is not None:
         if pos is None:
@@ -794,7 +802,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ta
     pt = _arg(table, "table", _I32, None, index)
     pl = _arg(lens, "lens", _I32, (R,), index)
     pc = None if cu is None else _arg(cu, "cu", _I32, (R + 1,), index)
-    ps = None if status is None else _arg(status, "status", _I32, None, index)
+    ps = None if status is None else _status(status, index)
     there = _elsewhere(q, stream)
     if there is not None:
         with there:

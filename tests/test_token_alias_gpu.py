@@ -144,3 +144,17 @@ def test_rope_refuses_an_output_on_itself(vx):  # noqa: F811
     for strides in ((0, 512, 64, 1), (1536, 64, 192, 1), (1536, 600, 70, 1)):
         out = room.as_strided(x.shape, strides)
         assert torch.equal(vx.rope(x, pos, f, out=out), vx.rope(x, pos, f))
+
+
+def test_status_words_have_an_element(vx):  # noqa: F811
+    """An empty status tensor has no address: what a call reports would be lost."""
+    lens, table, kp, vp = [20, 0, 7], i32(np.zeros((3, 4))), torch.zeros(4, 2, 32, 128, dtype=BF, device="cuda"), torch.zeros(4, 2, 32, 128, dtype=BF, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    q, k = torch.zeros(3, 8, 128, device="cuda").to(BF), torch.zeros(3, 2, 128, device="cuda").to(BF)
+    z = i32([0, 0, 0])
+    for call in (lambda: vx.paged_attn(q, kp, vp, table, i32(lens), status=none),
+                 lambda: vx.paged_append(k, k, z, kp, vp, status=none),
+                 lambda: vx.paged_plan(z, z, table, z, i32([0]), 32, 4, status=none),
+                 lambda: vx.paged_release(z, z, table, z, i32([0]), 32, status=none)):
+        with pytest.raises(ValueError, match="status"):
+            call()
