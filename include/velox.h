@@ -495,7 +495,8 @@ VELOX_API size_t velox_paged_attn_workspace_size(int R, int H, int Hkv, int d);
  *       8, max_pages * page <= 512 n and R * Hkv * ceil(H / Hkv / 16) * n <= 256
  * table and lens must not change during the call: results are then undefined (what is read
  * and written stays within the arguments).
- * A request of length 0 gets zeros, with lse = -inf. What lies in a page behind the
+ * A request of length 0 gets zeros, with lse = -inf; one whose scores are all -inf gets NaN, as
+ * a softmax of them, also with lse = -inf. What lies in a page behind the
  * last token may be anything, NaN too. Scores and softmax statistics are
  * float32; probabilities enter the tensor-core product as the sum of two bf16.
  * The history of every (request, key head) is split evenly over the GPU and
