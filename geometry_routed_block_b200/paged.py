@@ -91,7 +91,9 @@ class PagedCache:
                          lens_out=self.lens, free_count_out=self.free_count, status=self.status)
 
     def check(self) -> None:
-        """Waits for the GPU and raises if a call reported something since the last check."""
+        """Waits for the GPU, calls on all its streams, and raises if one reported something since
+        the last check."""
+        torch.cuda.synchronize(self.status.device)
         bits = int(self.status.item())
         self.status.zero_()
         if bits & vx.VELOX_STATUS_TIMEOUT:
