@@ -50,10 +50,10 @@ constexpr int BOX = 16;        // tokens that one load fetches: the smallest pag
 constexpr int NW = 4;          // warps per CTA
 constexpr int NT = NW * 32;
 constexpr int MAX_GRID = 320;  // CTAs at most
-// Bytes that the CTAs together keep in flight. More is slower, DRAM then serves too many
-// places at once: the whole history of 24 heads (2.77 GB) takes 411 us at 12 MB, 399 at 17,
-// 409 at 19, 411 at 21, 422 at 28 (in a steady loop, under the power cap, 406 at 17 and
-// 438 at 28); a ragged batch 91.9, 88.6, 90.4, 94.6, 92.3
+// Bytes that the CTAs together keep in flight, in whole units a warp. More is slower, DRAM then
+// serves too many places at once: the whole history of 24 heads (2.77 GB, clusters of 10) takes
+// 394 us with two units a warp (15.7 MB) and 427 with three (23.6 MB), in a steady loop under
+// the power cap 404 and 413; a ragged batch of 64 requests 78.4 (17.0 MB) and 81.9 (25.5 MB)
 constexpr double IN_FLIGHT = 17.5e6;
 constexpr int JT = 256;        // threads of the joining kernel
 constexpr int JW = JT / 32;
@@ -65,8 +65,8 @@ constexpr int MIN_SHARE = 2;
 // Where no row can be longer (by the width of the table) than so many tokens for each of the
 // n = 1, 2, 4 or 8 CTAs that every row can have at once, rows are not dealt out by length:
 // a CTA or a cluster takes a row, in one launch and without a workspace. 32 / 8 heads, one
-// request: 20 tokens 4.8 us, 257 tokens 6.5 us (one CTA a row 8.4, dealt out 9.1), 480 tokens 6.7
-// us (10.6, 9.2); 1024 tokens with one CTA a row 16.4 us, dealt out 9.4.
+// request, history in L2: 20 tokens 4.4 us (dealt out 6.9), 257 tokens 6.0 (one CTA a row 8.0,
+// dealt out 9.5), 480 tokens 6.4 (10.1, 8.9), 1024 tokens 7.2 (16.3, 8.9).
 constexpr int WHOLE_TOKENS = 512, WHOLE_CTAS = 256;
 
 template <int D, int MT>
@@ -134,8 +134,10 @@ __device__ __forceinline__ int Work::cta_of(long long u) const {
 __device__ __forceinline__ int weight(int units) { return units > 0 ? units + ROW_COST : 0; }
 
 // The row of q and o that request r attends with: its own number or, in a plan's STEP, that
-// of its last new token, -1 where it has none (`bad`: where there can be no such row). STEP is
-// a parameter of the kernels: asked at run time it cost calls without a plan 0.1 to 0.4 us.
+// of its last new token, -1 where it has none (`bad`: where there can be no such row). An idle
+// request counts as one without tokens: 64 ragged requests take 88 us, 58 with every second
+// one idle, 13 with 7 of 8. STEP is a parameter of the kernels: asked at run time it cost
+// calls without a plan 0.1 to 0.4 us.
 template <bool STEP>
 __device__ __forceinline__ int token_row(const PagedAttnArgs& a, int r, bool& bad) {
     if (!STEP) return r;
@@ -973,12 +975,13 @@ __global__ void __launch_bounds__(JT)
 }
 
 // CTAs per row where rows are not dealt out by length, else 0: those of a short history
-// (paged_attn_whole); a cluster for a single request, whose rows are all of one length, where clusters of 16,
-// 10 or 8 (sizes that the GPU holds at once, with two CTAs per SM) make up a grid that
-// fills it. 24 key heads, one launch and no workspace against two, in a steady loop: 4096
-// tokens 16.7 and 19.8 us, 32,768 tokens 67.7 and 70.3 us, 225,793 tokens 412 and 407 us
-// (clusters of 8: 16.4, 70.3, 455 us; of 11, which do not fit: 26.2, 103, 610 us). 8 key
-// heads (128 CTAs, not taken): 9.9 and 12.0 us at 4096 tokens, 195 and 148 us at 225,793.
+// (paged_attn_whole); a cluster for a single request, whose rows are all of one length, where
+// clusters of 16, 10 or 8 (sizes that the GPU holds at once, with two CTAs per SM) make up a
+// grid that fills it. 24 key heads, one launch against two: 4096 tokens (in L2) 12.6 and 15.5
+// us, 32,768 tokens 64.8 and 67.5, 225,793 tokens 389 and 403 (in a steady loop under the
+// power cap 402 and 406; clusters of 8: 13.0, 65.3, 412, steady 447; of 11, which do not fit:
+// 21.5, 100, 625). 8 key heads (128 CTAs, not taken): 10.4 and 12.1 us at 4096 tokens, 203 and
+// 141 at 225,793.
 // places(n): the device can place a cluster of n CTAs, more than the 8 that any can.
 template <typename F>
 int ctas_per_row(const PagedAttnArgs& a, long long rows, F places) {
@@ -1029,6 +1032,7 @@ int launch(const void* k_pages, const void* v_pages, PagedAttnArgs a, cudaStream
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return VELOX_ECUDA;
+    // a ragged batch of 64 requests: 78.4 us, 87.9 with one CTA per SM, 79.6 with two
     const int resident = std::min(7 * sms / 4, MAX_GRID);
     const long long rows = static_cast<long long>(a.R) * a.Hkv * a.head_tiles;
     const long long units = static_cast<long long>(a.max_pages) * a.page / C::UNIT + 1;

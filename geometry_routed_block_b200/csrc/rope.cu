@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(RT)
 
 // The half layout of bf16 rows: an item is 8 neighbours, and the other halves of its
 // pairs are an item of another lane of the warp and come from there. Rows are then
-// read and written whole, 256 bytes at a time at d = 128: 10.9 us for the queries of a
-// chunk, 13.7 us in two times 8 bytes a thread (float32, two times 16 bytes: 17.5 us so,
+// read and written whole, 256 bytes at a time at d = 128: 11.3 us for the queries of a
+// chunk, 13.7 us in two times 8 bytes a thread (float32, two times 16 bytes: 16.9 us so,
 // 21.5 us exchanged). Each lane of such a couple forms four of their eight angles.
 // A warp stays together for the exchange: who has no row only takes part in that.
 template <int U>
@@ -370,8 +370,8 @@ int launch(const RopeArgs& a, bool vec, cudaStream_t st) {
     if (gx >= (1ll << 31)) return VELOX_EINVAL;
     // The heads are split until there are two CTAs per SM, and no further than four heads
     // a thread, since each part forms its angles again. Queries of a chunk (24 heads of
-    // 4608 tokens, bf16): 9.3 us so, 10.9 us with four CTAs per SM; 200 tokens of 72
-    // heads 3.9 us, 4.9 us split to two heads
+    // 4608 tokens, bf16): 9.3 us so, 10.6 us with four CTAs per SM (half layout 11.3 and 12.3);
+    // 64 tokens of 72 heads 2.9 us, 3.5 us split to two heads
     const long long want = std::max<long long>(1, (296 + gx - 1) / gx);
     const int parts = static_cast<int>(std::min<long long>({want, (a.rows + 3) / 4, 65535}));
     const int rows_per_y = (a.rows + parts - 1) / parts;

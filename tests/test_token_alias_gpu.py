@@ -148,7 +148,8 @@ def test_rope_refuses_an_output_on_itself(vx):  # noqa: F811
 
 def test_status_words_have_an_element(vx):  # noqa: F811
     """An empty status tensor has no address: what a call reports would be lost."""
-    lens, table, kp, vp = [20, 0, 7], i32(np.zeros((3, 4))), torch.zeros(4, 2, 32, 128, dtype=BF, device="cuda"), torch.zeros(4, 2, 32, 128, dtype=BF, device="cuda")
+    lens, table = [20, 0, 7], i32(np.zeros((3, 4)))
+    kp, vp = (torch.zeros(4, 2, 32, 128, dtype=BF, device="cuda") for _ in range(2))
     none = torch.empty(0, dtype=torch.int32, device="cuda")
     q, k = torch.zeros(3, 8, 128, device="cuda").to(BF), torch.zeros(3, 2, 128, device="cuda").to(BF)
     z = i32([0, 0, 0])

@@ -23,17 +23,17 @@ CASES = {  # H, Hkv, d, page, lens, pages that the table is wider than it need b
 }
 
 
-@pytest.mark.parametrize("workspace", [True, False])
-@pytest.mark.parametrize("name", CASES)
+NEED_NONE = ("a CTA a row", "clusters of a short history")
+
+
+@pytest.mark.parametrize("name,workspace", [(n, True) for n in CASES] + [(n, False) for n in NEED_NONE])
 def test_expired_waits_report_timeout_and_write_nothing_else(vx, name, workspace):  # noqa: F811
     H, Hkv, d, page, lens, wider = CASES[name]
     R = len(lens)
     kp, vp, table, _ = attn_state(R, Hkv, d, page, lens, seed=H + d)
     table = np.concatenate([table, np.full((R, wider), -1)], 1)
     needs_none = vx._needs_no_workspace(R * Hkv * -(-H // Hkv // 16), table.shape[1] * page)
-    assert needs_none == (name in ("a CTA a row", "clusters of a short history"))
-    if not workspace and not needs_none:
-        pytest.skip("this size takes a workspace")
+    assert needs_none == (name in NEED_NONE)
     q = torch.randn(R, H, d, device="cuda").to(torch.bfloat16)
     t, n = i32(table), i32(lens)
     # a workspace of the size that the path needs: none at all, or what the library names
