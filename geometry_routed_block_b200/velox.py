@@ -606,9 +606,9 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
     """Pages for add [R] new tokens of requests with lens [R] cached ones: enters
     them in table [R,max_pages] and returns the step's PagedPlan with room for n_cap
     tokens (all int32). `out` gives the outputs' tensors; its lens and
-    free_count may be the inputs, so that a captured step carries its state on; else
-    the outputs share nothing with one another or the inputs. Tensors allocated here are
-    views of one buffer."""
+    free_count may be the inputs (lens also add), so that a captured step carries its
+    state on; else the outputs share nothing with one another or the inputs. Tensors
+    allocated here are views of one buffer."""
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pa = _arg(add, "add", _I32, (R,), index)
@@ -634,11 +634,10 @@ def paged_plan(add: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, free_
         oc, os_, op, oq, ol, of = [
             _arg(t, name, _I32, (size,), index) for t, name, size in
             zip(out, PagedPlan._fields, (R + 1, n_cap, n_cap, n_cap, R, 1))]
-        ins, outs = [("add", pa, R), ("free_list", pf, num_pages)], [
+        ins, outs = [("free_list", pf, num_pages)], [
             ("cu", oc, R + 1), ("slots", os_, n_cap), ("pos", op, n_cap), ("req", oq, n_cap),
             ("lens", ol, R), ("free_count", of, 1), ("table", pt, R * width), ("status", ps, 1)]
-        if ol != pl:
-            ins.append(("lens", pl, R))
+        ins += [(name, at, R) for name, at in (("lens", pl), ("add", pa)) if at != ol]
         if of != pc:
             ins.append(("free_count", pc, 1))
         _separate(ins, outs)
@@ -652,8 +651,8 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                   lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
                   status: torch.Tensor | None = None, stream=None):
     """The pages of the requests with done [R] != 0 go back on free_list (in
-    place); returns (lens, free_count) afterwards. The outputs may be the inputs, else they
-    share nothing with them; those allocated here are views of one buffer."""
+    place); returns (lens, free_count) afterwards. The outputs may be the inputs (lens_out
+    also done, which may be lens itself), else they share nothing with them; those allocated here are views of one buffer."""
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pd = _arg(done, "done", _I32, (R,), index)
@@ -671,9 +670,8 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
     ol = _arg(lens_out, "lens_out", _I32, (R,), index)
     of = _arg(free_count_out, "free_count_out", _I32, (1,), index)
     if given:
-        ins = [("done", pd, R), ("table", pt, R * width)]
-        if ol != pl:
-            ins.append(("lens", pl, R))
+        ins = [(name, at, R) for name, at in (("lens", pl), ("done", pd)) if at != ol]
+        ins.append(("table", pt, R * width))
         if of != pc:
             ins.append(("free_count", pc, 1))
         _separate(ins, [("lens_out", ol, R), ("free_count_out", of, 1), ("free_list", pf, num_pages),

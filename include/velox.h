@@ -407,8 +407,9 @@ VELOX_API int velox_rope(const void* x, int dtype, int B, int H, int N, int d, c
  *   lens  [R] int32     tokens already cached
  *   table [R][max_pages] int32   the new pages are entered behind the old ones
  *   free_list [num_pages], free_count [1] int32   the free pages (a stack)
- *   lens_out [R], free_count_out [1] int32 outputs; may be lens and free_count. Apart from
- *         that the outputs (table and status among them) share nothing with other arguments
+ *   lens_out [R], free_count_out [1] int32 outputs; may be lens (or add) and free_count.
+ *         Apart from that the outputs (table and status among them) share nothing with other
+ *         arguments
  *   cu    [R + 1] int32 output: request r's new tokens are cu[r] .. cu[r+1] - 1
  *   slots, pos, req [n_cap] int32 outputs: slot, position in its request and
  *         request of each new token, -1 from token cu[R] on; pos and req may be

@@ -32,7 +32,7 @@ def test_plan_refuses_shared_outputs(vx):  # noqa: F811
     bad = [  # what is put where
         (lens_room[:R], dict(lens=lens_room[1:])),          # one element further
         (lens_room[1:], dict(lens=lens_room[:R])),
-        (lens, dict(lens=add)), (lens, dict(free_count=lens[1:2])), (lens, dict(free_count=add[:1])),
+        (lens, dict(free_count=lens[1:2])), (lens, dict(free_count=add[:1])),
         (lens, dict(lens=table.view(-1)[:R])), (lens, dict(lens=fl[:R])),
         (lens, dict(slots=room[:n_cap], pos=room[n_cap - 1:2 * n_cap - 1])),
         (lens, dict(req=room[:n_cap], cu=room[n_cap - 1:n_cap + R])),
@@ -56,6 +56,28 @@ def test_plan_refuses_shared_outputs(vx):  # noqa: F811
     assert torch.equal(lens, want.lens) and torch.equal(fc, want.free_count) and status.item() == 0
 
 
+@pytest.mark.parametrize("R,n_cap", [(4, 80), (300, 5000), (2000, 30000)])
+def test_the_new_lengths_may_be_the_added_ones(vx, R, n_cap):  # noqa: F811
+    """Lengths doubled (add is lens is lens_out), written over add, and all that have tokens given back
+    (done is lens): one CTA, a cluster, and a grid with a second kernel."""
+    page, width = 16, 3
+    old = np.random.default_rng(R).integers(0, 12, R)
+    table, free, num = plan_state(old.tolist(), page, width, R, 1)
+    for over_add in (False, True):
+        lens, tab, fc = i32(old), i32(table), i32([len(free)])
+        fl, status = i32(free + [0] * (num - len(free))), i32([0])
+        add = lens.clone() if over_add else lens
+        want = vx.paged_plan(i32(old), i32(old), i32(table), fl, i32([len(free)]), page, n_cap)
+        out = plan_outputs(vx, R, n_cap, lens=add, free_count=fc)
+        vx.paged_plan(add, lens, tab, fl, fc, page, n_cap, out=out, status=status)
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+        now = add       # done, lens and lens_out at once
+        vx.paged_release(now, now, tab, fl, fc, page, lens_out=now, free_count_out=fc, status=status)
+        assert (now == 0).all() and fc.item() == num and status.item() == 0
+        assert sorted(fl.tolist()) == list(range(num))
+
+
 def test_release_refuses_shared_outputs(vx):  # noqa: F811
     R, page = 4, 16
     lens, table, fl, fc, num = cache_state()
@@ -63,7 +85,7 @@ def test_release_refuses_shared_outputs(vx):  # noqa: F811
     lens_room = torch.zeros(R + 1, dtype=torch.int32, device="cuda")
     lens_room[:R] = lens
     for src, kw in ((lens_room[:R], dict(lens_out=lens_room[1:])), (lens_room[1:], dict(lens_out=lens_room[:R])),
-                    (lens, dict(lens_out=done)), (lens, dict(lens_out=fl[:R])),
+                    (lens, dict(lens_out=fl[:R])),
                     (lens, dict(free_count_out=lens[:1])), (lens, dict(free_count_out=fl[-1:])),
                     (lens, dict(lens_out=table.view(-1)[:R])),
                     (lens, dict(lens_out=lens_room[:R], free_count_out=lens_room[1:2]))):
