@@ -652,7 +652,8 @@ def paged_release(done: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
                   status: torch.Tensor | None = None, stream=None):
     """The pages of the requests with done [R] != 0 go back on free_list (in
     place); returns (lens, free_count) afterwards. The outputs may be the inputs (lens_out
-    also done, which may be lens itself), else they share nothing with them; those allocated here are views of one buffer."""
+    also done, which may be lens itself), else they share nothing with them; those
+    allocated here are views of one buffer."""
     index = lens.get_device()
     R, width, num_pages, pl, pt, pf, pc = _pages_state(lens, table, free_list, free_count, index)
     pd = _arg(done, "done", _I32, (R,), index)
